@@ -39,6 +39,10 @@ __all__ = [
     "zero_host_adamw", "zero_host_threads",
     "OffloadStaging",
     "StepArgs", "dtype_code", "GLOBAL_BYTES",
+    "ZERO_STATE8_BLOCK", "ZERO_MAX_GROUPS", "state8_blocks", "zero_state8_encode",
+    "zero_state8_decode", "AdamGroup", "TensorSet", "zero_tensors_plan", "zero_tensors_step",
+    "zero_tensors_norm", "zero_tensors_apply", "zero_tensors_scalars", "XentArgs",
+    "zero_xent_workspace_bytes", "zero_xent_forward", "zero_xent_backward",
 ]
 
 GLOBAL_BYTES = ctypes.sizeof(zero_global_t)
@@ -519,3 +523,12 @@ def zero_gather_params(part: zero_partition_t, shards: Sequence, dtype, lo: int,
     sp = (_abi.vp * len(shards))(*[_dptr(t) for t in shards])
     check(lib().zero_gather_params(ctypes.byref(part), sp, dtype_code(dtype), lo, hi, _dptr(dst),
                                    _stream(stream)), "zero_gather_params")
+
+
+# ------------------------------------------------------ training operators
+# The second library (include/zero/train.h); it is loaded at the first call.
+from .train import (ZERO_MAX_GROUPS, ZERO_STATE8_BLOCK, AdamGroup, TensorSet,  # noqa: E402
+                    XentArgs, state8_blocks, zero_state8_decode, zero_state8_encode,
+                    zero_tensors_apply, zero_tensors_norm, zero_tensors_plan,
+                    zero_tensors_scalars, zero_tensors_step, zero_xent_backward,
+                    zero_xent_forward, zero_xent_workspace_bytes)

@@ -1,4 +1,5 @@
-"""Build the HIP library libzero_mi355x.so in place, for gfx950 only.
+"""Build the HIP libraries libzero_mi355x.so and libzero_train_mi355x.so in
+place, for gfx950 only.
 
     python -m zero_sharded_optimizer_step_amd.build
 
@@ -25,6 +26,12 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libzero_mi355x.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["zero_host.cpp", "zero_offload.cpp", "zero_kernels.hip"]
+# The training operators are a library of their own, so that the counter
+# records of the shard step, which are bound to libzero_mi355x.so's code,
+# stay valid when an operator changes.  It links to that library.
+TRAIN_LIB_NAME = "libzero_train_mi355x.so"
+TRAIN_LIB_PATH = os.path.join(PKG, TRAIN_LIB_NAME)
+TRAIN_SOURCES = ["train_host.cpp", "train_tensors.hip", "train_xent.hip"]
 ARCH = "gfx950"
 
 
@@ -44,10 +51,21 @@ def compile_flags() -> list[str]:
 
 
 def build(out: str = LIB_PATH, verbose: bool = False) -> str:
-    """Compile every source into one shared library (always recompiles)."""
+    """Compile the step's sources into one shared library (always
+    recompiles)."""
+    return _compile(SOURCES, [], out, verbose)
+
+
+def build_train(out: str = TRAIN_LIB_PATH, verbose: bool = False) -> str:
+    """Compile the training operators (always recompiles); they find
+    libzero_mi355x.so, built before, in their own directory."""
+    return _compile(TRAIN_SOURCES, ["-L", PKG, "-lzero_mi355x", "-Wl,-rpath,$ORIGIN"], out, verbose)
+
+
+def _compile(sources: list[str], link: list[str], out: str, verbose: bool) -> str:
     tmp = out + ".tmp%d" % os.getpid()
     cmd = [hipcc()] + compile_flags() + ["-shared"] + \
-        [os.path.join(CSRC, s) for s in SOURCES] + ["-o", tmp]
+        [os.path.join(CSRC, s) for s in sources] + link + ["-o", tmp]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -117,3 +135,4 @@ def code_hash(path: str = LIB_PATH) -> str:
 
 if __name__ == "__main__":
     print(build(verbose="-v" in sys.argv))
+    print(build_train(verbose="-v" in sys.argv))
