@@ -40,37 +40,48 @@ __device__ __forceinline__ void widen_quad(const typename GradQuad<DT>::T v, flo
         decode4<DT>(v, o);
     }
 }
-template <int DT>
-__device__ __forceinline__ float grad_elem(const void* base, int64_t i) {
-    if constexpr (DT == ZERO_FP32) return ZERO_GLOBAL(const float, base)[i];
-    else return lo_to_f32<DT>(ZERO_GLOBAL(const unsigned short, base)[i]);
-}
 
-// The quad of elements [e, e + 4) of a gradient of n elements, widened;
-// elements past the end are 0.
+// Quads of elements [e, e + 4) of n: whole where `full`, else the elements
+// there are, the rest 0.  What is loaded stays as it lies until it is used,
+// so that a thread's loads are all in flight together.
 template <int DT>
-__device__ __forceinline__ void load_grad(const void* base, int64_t e, int64_t n, float o[4]) {
-    typedef typename GradQuad<DT>::U U;
-    constexpr int kBytes = DT == ZERO_FP32 ? 4 : 2;
-    if (e + 4 <= n) {
-        widen_quad<DT>(*ZERO_GLOBAL(const U, static_cast<const char*>(base) + e * kBytes), o);
+__device__ __forceinline__ typename GradQuad<DT>::T load_grad(const void* base, int64_t e, int64_t n, bool full) {
+    typename GradQuad<DT>::T o = {};
+    if constexpr (DT == ZERO_FP32) {
+        const float* p = static_cast<const float*>(base) + e;
+        if (full) {
+            o = *ZERO_GLOBAL(const f32x4_any, p);
+        } else {
+            #pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (e + k < n) o[k] = ZERO_GLOBAL(const float, p)[k];
+        }
     } else {
-        #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = e + k < n ? grad_elem<DT>(base, e + k) : 0.0f;
-    }
-}
-__device__ __forceinline__ f32x4 load_f32(const float* base, int64_t e, int64_t n) {
-    f32x4 o;
-    if (e + 4 <= n) {
-        o = __builtin_nontemporal_load(ZERO_GLOBAL(const f32x4_any, base + e));
-    } else {
-        #pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = e + k < n ? ZERO_GLOBAL(const float, base)[e + k] : 0.0f;
+        const unsigned short* p = static_cast<const unsigned short*>(base) + e;
+        if (full) {
+            o = *ZERO_GLOBAL(const u32x2_any, p);
+        } else {
+            #pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (e + k < n)
+                    o[k / 2] |= static_cast<unsigned>(ZERO_GLOBAL(const unsigned short, p)[k]) << (16 * (k % 2));
+        }
     }
     return o;
 }
-__device__ __forceinline__ void store_f32(float* base, int64_t e, int64_t n, const f32x4 x) {
-    if (e + 4 <= n) {
+__device__ __forceinline__ f32x4 load_f32(const float* base, int64_t e, int64_t n, bool full) {
+    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (full) {
+        o = __builtin_nontemporal_load(ZERO_GLOBAL(const f32x4_any, base + e));
+    } else {
+        #pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (e + k < n) o[k] = ZERO_GLOBAL(const float, base)[e + k];
+    }
+    return o;
+}
+__device__ __forceinline__ void store_f32(float* base, int64_t e, int64_t n, bool full, const f32x4 x) {
+    if (full) {
         __builtin_nontemporal_store(x, ZERO_GLOBAL(f32x4_any, base + e));
     } else {
         #pragma unroll
@@ -79,9 +90,9 @@ __device__ __forceinline__ void store_f32(float* base, int64_t e, int64_t n, con
     }
 }
 template <int DT>
-__device__ __forceinline__ void store_16(void* base, int64_t e, int64_t n, const f32x4 x) {
+__device__ __forceinline__ void store_16(void* base, int64_t e, int64_t n, bool full, const f32x4 x) {
     unsigned short* p = static_cast<unsigned short*>(base) + e;
-    if (e + 4 <= n) {
+    if (full) {
         u32x2 o;
         o.x = pack2<DT>(x.x, x.y);
         o.y = pack2<DT>(x.z, x.w);
@@ -200,7 +211,8 @@ __global__ __launch_bounds__(256) void state8_encode_kernel(const float* __restr
     const int64_t b = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
     if (b * ZERO_STATE8_BLOCK >= n) return;            // whole waves
     const int64_t e = b * ZERO_STATE8_BLOCK + (threadIdx.x & 63) * 4;
-    const f32x4 mq = load_f32(m, e, n), vq = load_f32(v, e, n);
+    const bool full = e + 4 <= n;
+    const f32x4 mq = load_f32(m, e, n, full), vq = load_f32(v, e, n, full);
     encode_block<true>(mq, vq, 0, 0, state + b * 512, scale + b * 2);
 }
 
@@ -222,56 +234,101 @@ __global__ __launch_bounds__(256) void state8_decode_kernel(const unsigned char*
         vq[k] = decode_v((cv >> (8 * k)) & 255u, ev);
     }
     const int64_t e = b * ZERO_STATE8_BLOCK + lane * 4;
+    const bool full = e + 4 <= n;
     if constexpr (DT == ZERO_FP32) {
-        store_f32(static_cast<float*>(m), e, n, mq);
-        store_f32(static_cast<float*>(v), e, n, vq);
+        store_f32(static_cast<float*>(m), e, n, full, mq);
+        store_f32(static_cast<float*>(v), e, n, full, vq);
     } else {
-        store_16<DT>(m, e, n, mq);
-        store_16<DT>(v, e, n, vq);
+        store_16<DT>(m, e, n, full, mq);
+        store_16<DT>(v, e, n, full, vq);
     }
 }
 
 // ------------------------------------------------------------------ the norm
-// At most kFoldBlocks blocks walk the chunks together (block b's four groups
-// of 256 threads take chunks 4 b .. 4 b + 3 of every round), so the chunks in
-// flight stay one compact window; each block leaves one entry of a partials
-// slot.  Every sum has a fixed order.
+// At most kFoldBlocks blocks of 1024 threads walk the chunks together, 8
+// chunks a block and kNormUnroll such runs in flight, so what is in flight
+// stays one compact window; each block leaves one entry of a partials slot.
+// A wave takes half a chunk, 8 elements a lane.  All loads of a round are
+// issued before any is used: a half chunk that ends inside reads the table
+// instead, and its elements are taken one by one afterwards.  Every sum has
+// a fixed order.
 constexpr int kNormThreads = 1024;
-constexpr int kNormGroups = kNormThreads / kChunkThreads;
-constexpr int kNormUnroll = 4;
+constexpr int kNormRun = 8;                           // chunks of a block at a time
+constexpr int kNormUnroll = 8;
+constexpr int kHalf = kChunk / 2;
+static_assert(kNormThreads * 8 == kNormRun * kChunk, "8 elements a thread");
 
 template <int DT>
 __global__ __launch_bounds__(kNormThreads) void tensors_norm_kernel(
     const TensorRec* __restrict__ recs, const uint32_t* __restrict__ map, int64_t n_chunks,
     float inv_scale, const zero_tensors_scalars_t* __restrict__ sc, unsigned char* __restrict__ slot) {
+    constexpr int kWords = DT == ZERO_FP32 ? 2 : 1;    // 16-byte loads of 8 elements
+    typedef u32x4 words __attribute__((aligned(2)));
     if (sc) inv_scale = sc->inv_scale;
-    const int group = __builtin_amdgcn_readfirstlane(threadIdx.x / kChunkThreads);
-    const int tid = threadIdx.x % kChunkThreads;
-    const int64_t round = static_cast<int64_t>(gridDim.x) * kNormGroups;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int lane = threadIdx.x & 63;
+    const int64_t round = static_cast<int64_t>(gridDim.x) * kNormRun;
     double ss = 0.0;
     int bad = 0;
-    for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kNormGroups + group; c0 < n_chunks;
+    auto add = [&](float x) {
+        const float g = x * inv_scale;
+        bad |= !finite(g);
+        ss += static_cast<double>(g) * static_cast<double>(g);
+    };
+    for (int64_t c0 = static_cast<int64_t>(blockIdx.x) * kNormRun + wave / 2; c0 < n_chunks;
          c0 += round * kNormUnroll) {
-        float x[kNormUnroll][4];
+        const char* base[kNormUnroll];
+        int64_t left[kNormUnroll];                     // elements from this half chunk's first on
+        u32x4 x[kNormUnroll][kWords];
+        // in three sweeps, so that the scalar loads of a sweep overlap
+        uint32_t owner[kNormUnroll];
         #pragma unroll
         for (int u = 0; u < kNormUnroll; ++u) {
             const int64_t c = c0 + u * round;
-            if (c < n_chunks) {
-                const TensorRec& r = recs[map[c]];
-                load_grad<DT>(r.grad, (c - r.first_chunk) * kChunk + tid * kQuad, r.numel, x[u]);
-            } else {
-                #pragma unroll
-                for (int k = 0; k < 4; ++k) x[u][k] = 0.0f;
-            }
+            owner[u] = map[c < n_chunks ? c : n_chunks - 1];
+        }
+        int64_t numel[kNormUnroll], first[kNormUnroll];
+        #pragma unroll
+        for (int u = 0; u < kNormUnroll; ++u) {
+            const TensorRec& r = recs[owner[u]];
+            base[u] = static_cast<const char*>(r.grad);
+            numel[u] = r.numel;
+            first[u] = r.first_chunk;
         }
         #pragma unroll
-        for (int u = 0; u < kNormUnroll; ++u)
+        for (int u = 0; u < kNormUnroll; ++u) {
+            const int64_t c = c0 + u * round;
+            const int64_t e = (c - first[u]) * kChunk + (wave & 1) * kHalf;
+            base[u] += e * (DT == ZERO_FP32 ? 4 : 2);
+            left[u] = c < n_chunks ? numel[u] - e : 0;
+        }
+        #pragma unroll
+        for (int u = 0; u < kNormUnroll; ++u) {
+            const char* at = left[u] >= kHalf ? base[u] + lane * (16 * kWords) : reinterpret_cast<const char*>(recs);
             #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float g = x[u][k] * inv_scale;
-                bad |= !finite(g);
-                ss += static_cast<double>(g) * static_cast<double>(g);
+            for (int w = 0; w < kWords; ++w) x[u][w] = *ZERO_GLOBAL(const words, at + 16 * w);
+        }
+        #pragma unroll
+        for (int u = 0; u < kNormUnroll; ++u) {
+            if (left[u] >= kHalf) {
+                #pragma unroll
+                for (int w = 0; w < kWords; ++w)
+                    #pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (DT == ZERO_FP32) {
+                            add(__uint_as_float(x[u][w][k]));
+                        } else {
+                            add(lo_to_f32<DT>(x[u][w][k]));
+                            add(hi_to_f32<DT>(x[u][w][k]));
+                        }
+                    }
+            } else {
+                for (int64_t i = lane; i < left[u]; i += 64) {
+                    if constexpr (DT == ZERO_FP32) add(ZERO_GLOBAL(const float, base[u])[i]);
+                    else add(lo_to_f32<DT>(ZERO_GLOBAL(const unsigned short, base[u])[i]));
+                }
             }
+        }
     }
     block_reduce<kNormThreads>(ss, bad);
     if (threadIdx.x == 0) {
@@ -284,8 +341,8 @@ __global__ __launch_bounds__(kNormThreads) void tensors_norm_kernel(
     }
 }
 
-// The list's result from its slot, by one block of 256 threads; thread 0
-// holds it.
+// The list's result from its slot, by one block of 256 threads, for all of
+// them.
 static_assert(kFoldBlocks <= kChunkThreads, "one entry a thread");
 __device__ __forceinline__ zero_global_t fold_slot(const unsigned char* __restrict__ slot,
                                                    const zero_tensors_scalars_t& k,
@@ -300,12 +357,22 @@ __device__ __forceinline__ zero_global_t fold_slot(const unsigned char* __restri
         bad = p[threadIdx.x].flag;
     }
     block_reduce<kChunkThreads>(ss, bad);
+    __shared__ double s_total;
+    __shared__ int s_any;
+    if (threadIdx.x == 0) {
+        s_total = ss;
+        s_any = bad;
+    }
+    __syncthreads();
+    ss = s_total;
+    bad = s_any;
     double peer = k.peer_sumsq, max_norm = k.max_grad_norm;
     int peer_bad = k.peer_overflow;
     if (sc) {
-        peer = sc->peer_sumsq;
-        max_norm = sc->max_grad_norm;
-        peer_bad = sc->peer_overflow;
+        const auto* d = ZERO_CONSTANT(zero_tensors_scalars_t, sc);
+        peer = d->peer_sumsq;
+        max_norm = d->max_grad_norm;
+        peer_bad = d->peer_overflow;
     }
     ss += peer;
     bad |= peer_bad;
@@ -328,13 +395,17 @@ __global__ __launch_bounds__(kChunkThreads) void tensors_combine_kernel(
 }
 
 // ---------------------------------------------------------------- the update
-template <int GT, int PT, int BITS>
+// One thread per quad, one wave per block of an 8-bit state.  With FOLD the
+// block joins the norm's partials itself (4 KB from L2, behind its loads)
+// instead of reading a result that a launch in between made.
+template <int GT, int PT, int BITS, bool FOLD>
 __global__ __launch_bounds__(kChunkThreads) void tensors_apply_kernel(
     const TensorRec* __restrict__ recs, const uint32_t* __restrict__ map, int64_t last_chunk,
-    const zero_global_t* __restrict__ glob, zero_tensors_scalars_t k,
-    const zero_tensors_scalars_t* __restrict__ sc) {
-    if (glob->overflow) return;                        // skipped step: touch nothing
-    const float coef = glob->coef;
+    const zero_global_t* __restrict__ glob, const unsigned char* __restrict__ slot, zero_tensors_scalars_t k,
+    const zero_tensors_scalars_t* __restrict__ sc, zero_global_t* __restrict__ result) {
+    if constexpr (!FOLD) {
+        if (glob->overflow) return;                    // skipped step: touch nothing
+    }
     // from the end of the list: what the norm pass read last may still be
     // in the last-level cache
     const int64_t chunk = last_chunk - static_cast<int64_t>(blockIdx.x);
@@ -355,51 +426,67 @@ __global__ __launch_bounds__(kChunkThreads) void tensors_apply_kernel(
     const int64_t in_tensor = (chunk - r.first_chunk) * kChunk;
     const int64_t e = in_tensor + threadIdx.x * kQuad;
     const int64_t n = r.numel;
-    if constexpr (BITS == 32) {
-        if (e >= n) return;
-    } else {
-        if (in_tensor + (threadIdx.x & ~63u) * kQuad >= n) return;   // whole waves
+    const bool full = e + kQuad <= n;
+    // a wave with no element; within FOLD it still joins the block's fold
+    const bool idle = in_tensor + (threadIdx.x & ~63u) * kQuad >= n;
+    if constexpr (!FOLD) {
+        if (idle) return;
     }
-    float g[4];
-    load_grad<GT>(r.grad, e, n, g);
-    f32x4 p = load_f32(r.master, e, n), m, v;
-    unsigned char* state = nullptr;
-    unsigned char* scale = nullptr;
-    uint32_t place = 0;
-    if constexpr (BITS == 32) {
-        m = load_f32(static_cast<const float*>(r.m), e, n);
-        v = load_f32(static_cast<const float*>(r.v), e, n);
+    typename GradQuad<GT>::T gq = {};
+    f32x4 p = {}, m = {}, v = {};
+    uint32_t cm = 0, cv = 0, es = 0;
+    const int lane = threadIdx.x & 63;
+    const int64_t b = in_tensor / ZERO_STATE8_BLOCK + (threadIdx.x >> 6);
+    unsigned char* state = static_cast<unsigned char*>(r.m) + b * 512;
+    unsigned char* scale = static_cast<unsigned char*>(r.v) + b * 2;
+    if (!idle) {
+        gq = load_grad<GT>(r.grad, e, n, full);
+        p = load_f32(r.master, e, n, full);
+        if constexpr (BITS == 32) {
+            m = load_f32(static_cast<const float*>(r.m), e, n, full);
+            v = load_f32(static_cast<const float*>(r.v), e, n, full);
+        } else {
+            const auto* s = ZERO_GLOBAL(const uint32_t, state);
+            cm = __builtin_nontemporal_load(s + lane);
+            cv = __builtin_nontemporal_load(s + 64 + lane);
+            es = *ZERO_GLOBAL(const unsigned short, scale);
+        }
+    }
+    float coef;
+    if constexpr (FOLD) {
+        const zero_global_t o = fold_slot(slot, k, sc);
+        if (blockIdx.x == 0 && threadIdx.x == 0) *result = o;
+        if (idle || o.overflow) return;
+        coef = o.coef;
     } else {
-        const int64_t b = in_tensor / ZERO_STATE8_BLOCK + (threadIdx.x >> 6);
-        const int lane = threadIdx.x & 63;
-        state = static_cast<unsigned char*>(r.m) + b * 512;
-        scale = static_cast<unsigned char*>(r.v) + b * 2;
-        const auto* s = ZERO_GLOBAL(const uint32_t, state);
-        const uint32_t cm = __builtin_nontemporal_load(s + lane), cv = __builtin_nontemporal_load(s + 64 + lane);
-        const uint32_t es = *ZERO_GLOBAL(const unsigned short, scale);
+        coef = glob->coef;
+    }
+    if constexpr (BITS == 8) {
         const int em = es & 255, ev = es >> 8;
         #pragma unroll
         for (int j = 0; j < 4; ++j) {
             m[j] = decode_m((cm >> (8 * j)) & 255u, em);
             v[j] = decode_v((cv >> (8 * j)) & 255u, ev);
         }
-        place = (r.first_block + static_cast<uint32_t>(b)) * ZERO_STATE8_BLOCK + lane * kQuad;
     }
+    float g[4];
+    widen_quad<GT>(gq, g);
     #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float pe = p[j], me = m[j], ve = v[j];
         adamw1((g[j] * inv_scale) * coef, pe, me, ve, c);
         p[j] = pe; m[j] = me; v[j] = ve;
     }
-    store_f32(r.master, e, n, p);
+    store_f32(r.master, e, n, full, p);
     if constexpr (BITS == 32) {
-        store_f32(static_cast<float*>(r.m), e, n, m);
-        store_f32(static_cast<float*>(r.v), e, n, v);
+        store_f32(static_cast<float*>(r.m), e, n, full, m);
+        store_f32(static_cast<float*>(r.v), e, n, full, v);
     } else {
         // padding stays zero: its gradient and codes are
+        const uint32_t place = (r.first_block + static_cast<uint32_t>(b)) * ZERO_STATE8_BLOCK + lane * kQuad;
         encode_block<false>(m, v, place, key, state, scale);
     }
-    if constexpr (PT != 0) store_16<PT>(r.param, e, n, p);
+    if constexpr (PT != 0) store_16<PT>(r.param, e, n, full, p);
 }
 
 // ------------------------------------------------------------------ launches
@@ -412,6 +499,11 @@ int launch_error(const char* what) {
 // Chunks of one launch: a grid holds fewer than 2^32 threads.
 constexpr int64_t kLaunchChunks = int64_t(1) << 23;
 static_assert(kLaunchChunks * kChunkThreads < (int64_t(1) << 32), "threads of one launch");
+
+// Up to here the update's blocks are all on the chip at once, so each joining
+// the norm's partials costs about a microsecond once, less than the launch of
+// a kernel that joins them (2 us and the gap before it).
+constexpr int64_t kFoldChunks = 2048;
 
 struct Table {
     const TensorRec* recs;
@@ -426,7 +518,7 @@ Table table_of(const zero_tensors_args* a) {
 
 int launch_norm(const zero_tensors_args* a, const zero_tensors_scalars_t& k, unsigned char* slot, hipStream_t st) {
     const Table t = table_of(a);
-    int64_t blocks = (t.n_chunks + kNormGroups - 1) / kNormGroups;
+    int64_t blocks = (t.n_chunks + kNormRun - 1) / kNormRun;
     blocks = blocks < 1 ? 1 : (blocks > kFoldBlocks ? kFoldBlocks : blocks);
 #define ZERO_NORM(DT)                                                                                    \
     hipLaunchKernelGGL((tensors_norm_kernel<DT>), dim3(static_cast<unsigned>(blocks)), dim3(kNormThreads), 0, \
@@ -440,38 +532,49 @@ int launch_norm(const zero_tensors_args* a, const zero_tensors_scalars_t& k, uns
     return launch_error("list norm kernel launch");
 }
 
-template <int GT, int PT>
-void launch_apply_types(const zero_tensors_args* a, const zero_tensors_scalars_t& k, const zero_global_t* glob,
-                        hipStream_t st) {
+// Where the update finds the step's result: already joined in glob, or (glob
+// NULL) as the partials of `slot`, which it then joins and writes to result.
+struct Found {
+    const zero_global_t* glob;
+    const unsigned char* slot;
+    zero_global_t* result;
+};
+
+template <int GT, int PT, int BITS>
+void launch_apply_types(const zero_tensors_args* a, const zero_tensors_scalars_t& k, const Found& f, hipStream_t st) {
     const Table t = table_of(a);
     for (int64_t last = t.n_chunks - 1; last >= 0; last -= kLaunchChunks) {
         const dim3 grid(static_cast<unsigned>(last + 1 < kLaunchChunks ? last + 1 : kLaunchChunks));
-        if (a->plan.state_bits == 8)
-            hipLaunchKernelGGL((tensors_apply_kernel<GT, PT, 8>), grid, dim3(kChunkThreads), 0, st, t.recs, t.map,
-                               last, glob, k, a->scalars);
+        if (f.glob)
+            hipLaunchKernelGGL((tensors_apply_kernel<GT, PT, BITS, false>), grid, dim3(kChunkThreads), 0, st, t.recs,
+                               t.map, last, f.glob, f.slot, k, a->scalars, f.result);
         else
-            hipLaunchKernelGGL((tensors_apply_kernel<GT, PT, 32>), grid, dim3(kChunkThreads), 0, st, t.recs, t.map,
-                               last, glob, k, a->scalars);
+            hipLaunchKernelGGL((tensors_apply_kernel<GT, PT, BITS, true>), grid, dim3(kChunkThreads), 0, st, t.recs,
+                               t.map, last, f.glob, f.slot, k, a->scalars, f.result);
     }
+}
+
+template <int GT, int PT>
+void launch_apply_bits(const zero_tensors_args* a, const zero_tensors_scalars_t& k, const Found& f, hipStream_t st) {
+    if (a->plan.state_bits == 8) launch_apply_types<GT, PT, 8>(a, k, f, st);
+    else launch_apply_types<GT, PT, 32>(a, k, f, st);
 }
 
 template <int GT>
-void launch_apply_grad(const zero_tensors_args* a, const zero_tensors_scalars_t& k, const zero_global_t* glob,
-                       hipStream_t st) {
+void launch_apply_grad(const zero_tensors_args* a, const zero_tensors_scalars_t& k, const Found& f, hipStream_t st) {
     switch (a->plan.param_dtype) {
-        case ZERO_BF16: launch_apply_types<GT, ZERO_BF16>(a, k, glob, st); break;
-        case ZERO_FP16: launch_apply_types<GT, ZERO_FP16>(a, k, glob, st); break;
-        default: launch_apply_types<GT, 0>(a, k, glob, st); break;
+        case ZERO_BF16: launch_apply_bits<GT, ZERO_BF16>(a, k, f, st); break;
+        case ZERO_FP16: launch_apply_bits<GT, ZERO_FP16>(a, k, f, st); break;
+        default: launch_apply_bits<GT, 0>(a, k, f, st); break;
     }
 }
 
-int launch_apply(const zero_tensors_args* a, const zero_tensors_scalars_t& k, const zero_global_t* glob,
-                 hipStream_t st) {
+int launch_apply(const zero_tensors_args* a, const zero_tensors_scalars_t& k, const Found& f, hipStream_t st) {
     if (a->plan.n_chunks == 0) return ZERO_OK;
     switch (a->plan.grad_dtype) {
-        case ZERO_BF16: launch_apply_grad<ZERO_BF16>(a, k, glob, st); break;
-        case ZERO_FP16: launch_apply_grad<ZERO_FP16>(a, k, glob, st); break;
-        default: launch_apply_grad<ZERO_FP32>(a, k, glob, st); break;
+        case ZERO_BF16: launch_apply_grad<ZERO_BF16>(a, k, f, st); break;
+        case ZERO_FP16: launch_apply_grad<ZERO_FP16>(a, k, f, st); break;
+        default: launch_apply_grad<ZERO_FP32>(a, k, f, st); break;
     }
     return launch_error("list update kernel launch");
 }
@@ -553,7 +656,8 @@ int zero_tensors_apply(const zero_tensors_args* a, const void* global_dev, void*
     if (rc) return rc;
     if (!global_dev) return fail(ZERO_EINVAL, "global_dev is NULL");
     if (!aligned16(global_dev)) return fail(ZERO_EALIGN, "global_dev is not 16-byte aligned");
-    return launch_apply(a, k, static_cast<const zero_global_t*>(global_dev), static_cast<hipStream_t>(stream));
+    return launch_apply(a, k, {static_cast<const zero_global_t*>(global_dev), nullptr, nullptr},
+                        static_cast<hipStream_t>(stream));
 }
 
 int zero_tensors_step(const zero_tensors_args* a, zero_step_info* info, void* stream) {
@@ -564,9 +668,14 @@ int zero_tensors_step(const zero_tensors_args* a, zero_step_info* info, void* st
     hipStream_t st = static_cast<hipStream_t>(stream);
     unsigned char* slot = static_cast<unsigned char*>(a->workspace);
     if ((rc = launch_norm(a, k, slot, st))) return rc;
-    hipLaunchKernelGGL(tensors_combine_kernel, dim3(1), dim3(kChunkThreads), 0, st, slot, k, a->scalars, a->result);
-    if ((rc = launch_error("list combine kernel launch"))) return rc;
-    if ((rc = launch_apply(a, k, a->result, st))) return rc;
+    if (a->plan.n_chunks > 0 && a->plan.n_chunks <= kFoldChunks) {
+        if ((rc = launch_apply(a, k, {nullptr, slot, a->result}, st))) return rc;
+    } else {
+        hipLaunchKernelGGL(tensors_combine_kernel, dim3(1), dim3(kChunkThreads), 0, st, slot, k, a->scalars,
+                           a->result);
+        if ((rc = launch_error("list combine kernel launch"))) return rc;
+        if ((rc = launch_apply(a, k, {a->result, nullptr, nullptr}, st))) return rc;
+    }
     if (info) {
         hipError_t e = hipMemcpyAsync(info, a->result, sizeof(zero_global_t), hipMemcpyDeviceToHost, st);
         if (e == hipSuccess) e = hipStreamSynchronize(st);
