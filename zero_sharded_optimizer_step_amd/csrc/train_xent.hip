@@ -16,6 +16,9 @@
 // nothing is ever transposed in memory.
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+#include <utility>
+
 #include "train_internal.h"
 #include "zero_device.h"
 
@@ -30,6 +33,7 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 #define ZERO_LDS __attribute__((address_space(3)))
 
 constexpr int kTileK = 64;
+constexpr int kCus = 256, kLdsBytes = 160 << 10;
 constexpr uint32_t kNowhere = 0x80000000u;   // past every descriptor: loads 0
 
 enum Layout { kRows, kCols };   // the operand's rows lie along k, or k is the row
@@ -49,7 +53,7 @@ struct Product {
     int64_t lda, ldb;         // bytes from row to row
     int32_t m, n, k;          // extents; along a kCols operand's m or n whole 16 bytes are read
     int32_t tiles_m, tiles_n;
-    int32_t slice;            // k of one slice, a multiple of kTileK
+    int32_t slices, slice;    // slices of k, and k of one: a multiple of kTileK
     // epilogues
     char* c;                  // P, slabs or gradient
     int64_t ldc;              // elements
@@ -67,6 +71,14 @@ struct Product {
     int32_t vocab;
 };
 
+// f(0), f(1) .. f(N - 1), each number a constant.
+template <int... I, typename F>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, const F& f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(const F& f) { each_of(std::make_integer_sequence<int, N>{}, f); }
+
 // Where 16-byte piece c of a tile's row lies: rows-along-k tiles (8 pieces a
 // row) swap pieces by the row, so that 16 lanes reading one piece of 16 rows
 // meet 16 different 16-byte bank groups; k-as-row tiles swap pairs of pieces
@@ -74,15 +86,22 @@ struct Product {
 __device__ __forceinline__ int swap_rows(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swap_cols(int k) { return ((k & 3) | ((k >> 1) & 4)) << 1; }
 
+// c += a b, in place: 64 accumulators fill the accumulation registers, and
+// left to the compiler's own allocation they wander through copies.
 template <int DT>
-__device__ __forceinline__ f32x4 mfma(const s16x8 a, const s16x8 b, const f32x4 c) {
-    if constexpr (DT == ZERO_BF16)
-        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-    else
-        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
-                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+__device__ __forceinline__ void mfma(f32x4& c, const s16x8 a, const s16x8 b) {
+    if constexpr (DT == ZERO_BF16) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    else asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
+
+// Element e of an accumulator, taken here: the compiler's own copies move all
+// 256 at once and spill what stands in their way.
+__device__ __forceinline__ float taken(const f32x4& c, int e) {
+    float o;
+    asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(o) : "a"(c[e]));
+    return o;
+}
+__device__ __forceinline__ f32x4 taken(const f32x4& c) { return f32x4{taken(c, 0), taken(c, 1), taken(c, 2), taken(c, 3)}; }
 
 // One operand's tile of R rows (m or n) by kTileK: this thread's share of
 // the loads into LDS, and its fragments out of it.
@@ -93,59 +112,79 @@ struct Operand {
     static constexpr int kLoads = (kPieces + THREADS - 1) / THREADS;
     static constexpr int kRowPieces = L == kRows ? kTileK / 8 : R / 8;
     static constexpr int kRowsALoad = THREADS / kRowPieces;
-    // a thread's later loads are the same piece of later rows
-    static_assert(kLoads == 1 || kRowsALoad % 16 == 0, "swaps repeat every 16 rows");
-    uint32_t off;             // of the first piece, or kNowhere
+    // a thread's later loads are the same piece of later rows, or in turn two pieces
+    static_assert(kLoads == 1 || kRowsALoad % 8 == 0, "swaps repeat every 16 rows");
+    static constexpr bool kTwo = L == kCols && kLoads > 1 && kRowsALoad % 16 != 0;
+    uint32_t off, off1;       // of the even and the odd loads' piece, or kNowhere
     int32_t along;            // kRows: its first k
     uint32_t next;            // bytes from load to load
-    int64_t row, rows;        // bytes of a row; kRows: of the rows from the tile's first on
+    int64_t row;              // bytes of a row
+    const char* base;         // the tile's first byte
+    int64_t bytes;            // from there to the end of its rows (kRows), of k (kCols)
 
-    __device__ __forceinline__ void setup(int64_t ld, int rows_left) {
+    // `p`: the operand at this slice's first k and the tile's first row or column r0.
+    __device__ __forceinline__ void setup(const char* p, int64_t ld, int rows_left, int r0, int k_lo, int k) {
         const int r = threadIdx.x / kRowPieces, c = threadIdx.x % kRowPieces;
         row = ld;
         next = static_cast<uint32_t>(kRowsALoad * ld);
+        base = p;
         if constexpr (L == kRows) {
             const int piece = c ^ swap_rows(r);
             off = static_cast<uint32_t>(r * ld + piece * 16);
             along = piece * 8;
-            rows = rows_left * ld;
+            bytes = rows_left * ld - k_lo * 2;
         } else {
             const int piece = c ^ swap_cols(r);
             off = piece * 8 < rows_left ? static_cast<uint32_t>(r * ld + piece * 16) : kNowhere;
+            const int other = c ^ swap_cols(r + kRowsALoad);
+            off1 = other * 8 < rows_left ? static_cast<uint32_t>(r * ld + other * 16) : kNowhere;
+            bytes = k * ld - r0 * 2;
         }
     }
-    // `base`: the tile's first byte at this step of k, `into` bytes into its
-    // row; k_left: k from here on.  The descriptor ends with the last row, so
-    // rows past it load 0; so does a piece of k past the end.
-    __device__ __forceinline__ void load(const char* base, int64_t into, int k_left, ZERO_LDS char* lds) const {
-        int64_t bytes = (L == kRows ? rows : k_left * row) - into;
-        bytes = bytes < 0x7ffffff0 ? bytes : 0x7ffffff0;
-        const __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<char*>(base), 0, static_cast<int>(bytes), 0x00020000);
+    // What the loads of one step need.  The descriptor ends with the last row
+    // (kRows) or the last k (kCols): rows past it load 0; so does a piece of k
+    // past the end.
+    struct Step {
+        const char* at;
+        int bytes;
+        uint32_t o, o1;
+    };
+    __device__ __forceinline__ Step step(int t, int k) const {
+        Step s;
+        int64_t left = L == kRows ? bytes : bytes - t * (kTileK * row);
+        left = left < 0 ? 0 : (left < 0x7ffffff0 ? left : 0x7ffffff0);
+        s.at = L == kRows ? base : base + t * (kTileK * row);
+        s.bytes = static_cast<int>(left);
+        // a tile's 256 rows of at most 4 MB end before kNowhere
+        s.o = L == kCols ? off : (along + t * kTileK < k ? off + t * (kTileK * 2) : kNowhere);
+        s.o1 = kTwo ? off1 : s.o;
+        return s;
+    }
+    __device__ __forceinline__ void load(const Step& s, ZERO_LDS char* lds, int j) const {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
         if constexpr (kPieces < THREADS) {
             if (wave * 64 >= kPieces) return;
         }
-        uint32_t o = L == kCols || along < k_left ? off : kNowhere;
-        #pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (ZERO_LDS void*)(lds + (j * THREADS + wave * 64) * 16),
-                                                     16, o, 0, 0, 0);
-            o += next;
-        }
+        const __amdgpu_buffer_rsrc_t r =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(s.at), 0, s.bytes, 0x00020000);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (ZERO_LDS void*)(lds + (j * THREADS + wave * 64) * 16), 16,
+                                                 (j % 2 ? s.o1 : s.o) + j * next, 0, 0, 0);
     }
-    // Lane l's 8 values of the fragment at row r0 (a multiple of 16), half h
-    // of the tile's k: row r0 + l % 16, k = 32 h + 8 (l / 16) + 0..7.
-    __device__ __forceinline__ static s16x8 fragment(const ZERO_LDS char* lds, int r0, int h) {
+    // Lane l's 8 values of fragment i of the wave whose rows start at r0, half
+    // h of the tile's k, are row r0 + 16 i + l % 16, k = 32 h + 8 (l / 16) +
+    // 0..7.  `first` is where those of i = h = 0 lie in the tile.
+    __device__ __forceinline__ static uint32_t first(int r0) {
         const int l = threadIdx.x & 63, s = l & 15, g = l >> 4;
+        if constexpr (L == kRows) return (r0 + s) * (kTileK * 2) + (g ^ swap_rows(s)) * 16;
+        // the 16 lanes of group g give 4 rows of k by 16 of m and get them turned
+        const int k = g * 8 + (s >> 2);
+        return k * (R * 2) + ((r0 / 16) ^ (swap_cols(k) >> 1)) * 32 + (s & 3) * 8;
+    }
+    __device__ __forceinline__ static s16x8 fragment(const ZERO_LDS char* lds, uint32_t first, int i, int h) {
         if constexpr (L == kRows) {
-            const int c = (h * 4 + g) ^ swap_rows(s);
-            return *(const ZERO_LDS s16x8*)(lds + (r0 + s) * (kTileK * 2) + c * 16);
+            return *(const ZERO_LDS s16x8*)(lds + (first ^ (h * 64)) + i * (16 * kTileK * 2));
         } else {
-            // the 16 lanes of group g give 4 rows of k by 16 of m and get them turned
-            const int k = h * 32 + g * 8 + (s >> 2);
-            const int u = (r0 / 16) ^ (swap_cols(k) >> 1);
-            const ZERO_LDS char* at = lds + k * (R * 2) + u * 32 + (s & 3) * 8;
+            const ZERO_LDS char* at = lds + (first ^ (i * 32)) + h * (32 * R * 2);
             const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZERO_LDS s16x4*)at);
             const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ZERO_LDS s16x4*)(at + 4 * R * 2));
             return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
@@ -153,206 +192,391 @@ struct Operand {
     }
 };
 
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr int kNotKept = INT32_MIN;
+
+// As the instruction has it: a NaN beside a number gives the number.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float o;
+    asm("v_max3_f32 %0, %1, %2, %3" : "=v"(o) : "v"(a), "v"(b), "v"(c));
+    return o;
+}
+// {x of the lane's even row of 16, x of its odd row}, {of the lower half, of the upper}
+__device__ __forceinline__ f32x2 other_row(float x) {
+    const auto o = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return f32x2{__uint_as_float(o[0]), __uint_as_float(o[1])};
+}
+__device__ __forceinline__ f32x2 other_half(float x) {
+    const auto o = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return f32x2{__uint_as_float(o[0]), __uint_as_float(o[1])};
+}
+// Is element `at` (16 i + e) among a lane's FM x 4?  And the element itself.
+template <int FM>
+__device__ __forceinline__ bool here(int at) { return (at & ~((FM - 1) * 16 + 3)) == 0; }
+template <int FM>
+__device__ __forceinline__ float pick(const f32x4 (&x)[FM], int at) {
+    float v[FM];
+    const bool b0 = at & 1, b1 = at & 2;
+    #pragma unroll
+    for (int i = 0; i < FM; ++i) {
+        const float lo = b0 ? x[i][1] : x[i][0], hi = b0 ? x[i][3] : x[i][2];
+        v[i] = b1 ? hi : lo;
+    }
+    #pragma unroll
+    for (int w = 1; w < FM; w *= 2) {
+        const bool b = at & (16 * w);
+        #pragma unroll
+        for (int i = 0; i < FM; i += 2 * w) v[i] = b ? v[i + w] : v[i];
+    }
+    return v[0];
+}
+// Two fragments' values one above the other in m, times f, in 16 bits: a lane
+// gives 4 consecutive m of each and gets 8 of one, for 16-byte stores.
+template <int DT>
+__device__ __forceinline__ u32x4 pair(const f32x4 a, const f32x4 b, float f) {
+    const auto lo = __builtin_amdgcn_permlane16_swap(pack2<DT>(a[0] * f, a[1] * f), pack2<DT>(b[0] * f, b[1] * f),
+                                                     false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(pack2<DT>(a[2] * f, a[3] * f), pack2<DT>(b[2] * f, b[3] * f),
+                                                     false, false);
+    return u32x4{lo[0], hi[0], lo[1], hi[1]};
+}
 __device__ __forceinline__ bool infinite(float x) { return __builtin_fabsf(x) == __builtin_inff(); }
 
+// The product's tile by tile.  What bounds a large one is the matrix cores'
+// power: at 4096 tokens x 4096 x 128000 in bf16 the clock falls to 1.8 GHz,
+// and the forward takes 2.99 ms (1.44 PFLOP/s) with values of a normal
+// distribution and 2.56 ms with zeros.  Hence
+//   - four waves with 128 x 128 of a 256 x 256 tile each, one a SIMD, so that
+//     a value out of LDS serves 8 products of 16 x 16 x 32 (eight waves of
+//     128 x 64 read half as much again: 3.35 ms with all of the below lacking);
+//   - the accumulators in the 256 accumulation registers, both halves'
+//     fragments in the others, every product with at most one other
+//     instruction behind it (in clumps of eight: 3.40 ms);
+//   - five slots of LDS for the operands' steps of 64 k, so a step's loads
+//     have one to three halves of a step to arrive and no wait drains them;
+//   - blocks that stay: a tile's first loads run under the epilogue of the
+//     tile before (as separate blocks, and with an epilogue that spilled
+//     registers: 3.10 ms).
 template <int DT, Layout LA, Layout LB, Epilogue E, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) {
     constexpr int kThreads = WM * WN * 64;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;     // fragments of a wave
     typedef Operand<LA, BM, kThreads> OpA;
     typedef Operand<LB, BN, kThreads> OpB;
-    __shared__ __attribute__((aligned(1024))) char a0[BM * kTileK * 2];
-    __shared__ __attribute__((aligned(1024))) char b0[BN * kTileK * 2];
-    __shared__ __attribute__((aligned(1024))) char a1[BM * kTileK * 2];
-    __shared__ __attribute__((aligned(1024))) char b1[BN * kTileK * 2];
+    constexpr int kSlot = (BM > BN ? BM : BN) * kTileK * 2;
+    __shared__ __attribute__((aligned(1024))) char s0[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s1[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s2[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s3[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s4[kSlot];
 
-    // Each XCD takes a contiguous run of tiles, ordered in strips of 4 along
-    // n, so the tiles its 32 CUs hold at a time share rows of both operands.
-    const int tiles = q.tiles_m * q.tiles_n;
-    int id = blockIdx.x;
-    {
+    // The grid is what the chip holds at once; a block walks the tiles of all
+    // slices.
+    const int tiles = q.tiles_m * q.tiles_n, total = tiles * q.slices;
+    struct Place {
+        int tm, m0, n0, slice, k_lo, k;                    // k: this slice's
+    };
+    auto place = [&](int id) -> Place {
+        Place w;
+        w.slice = id / tiles;
+        id -= w.slice * tiles;
+        // Each XCD takes a contiguous run of tiles, ordered in strips of 4 along
+        // n, so the tiles its 32 CUs hold at a time share rows of both operands.
         const int per = tiles / kXcds, extra = tiles % kXcds;
         const int x = id % kXcds, i = id / kXcds;
         id = x * per + (x < extra ? x : extra) + i;
-    }
-    constexpr int kStrip = 4;
-    const int strip = id / (kStrip * q.tiles_m);
-    const int width = q.tiles_n - strip * kStrip < kStrip ? q.tiles_n - strip * kStrip : kStrip;
-    const int in_strip = id - strip * kStrip * q.tiles_m;
-    const int tn = strip * kStrip + in_strip % width, tm = in_strip / width;
-    const int m0 = tm * BM, n0 = tn * BN;
+        constexpr int kStrip = 4;
+        const int strip = id / (kStrip * q.tiles_m);
+        const int width = q.tiles_n - strip * kStrip < kStrip ? q.tiles_n - strip * kStrip : kStrip;
+        const int in_strip = id - strip * kStrip * q.tiles_m;
+        w.tm = in_strip / width;
+        w.m0 = w.tm * BM;
+        w.n0 = (strip * kStrip + in_strip % width) * BN;
+        w.k_lo = w.slice * q.slice;
+        w.k = (q.k < w.k_lo + q.slice ? q.k : w.k_lo + q.slice) - w.k_lo;
+        w.k = w.k > 0 ? w.k : 0;
+        return w;
+    };
 
-    const int k_lo = static_cast<int>(blockIdx.y) * q.slice;
-    const int k_hi = q.k < k_lo + q.slice ? q.k : k_lo + q.slice;
-    const int steps = k_hi > k_lo ? (k_hi - k_lo + kTileK - 1) / kTileK : 0;
+    const int lane = threadIdx.x & 63, nl = lane & 15, ml = (lane >> 4) * 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
 
     OpA oa;
     OpB ob;
-    oa.setup(q.lda, q.m - m0);
-    ob.setup(q.ldb, q.n - n0);
-    // bytes from one step of k to the next
-    const int64_t sa = LA == kRows ? kTileK * 2 : kTileK * q.lda;
-    const int64_t sb = LB == kRows ? kTileK * 2 : kTileK * q.ldb;
-    const char* pa = q.a + (LA == kRows ? m0 * q.lda + k_lo * 2 : k_lo * q.lda + m0 * 2);
-    const char* pb = q.b + (LB == kRows ? n0 * q.ldb + k_lo * 2 : k_lo * q.ldb + n0 * 2);
-
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int wm = (wave % WM) * (BM / WM), wn = (wave / WM) * (BN / WN);
+    Place w;
+    auto load = [&](const auto& op, int t, char* to) -> void {
+        const auto st = op.step(t, w.k);
+        #pragma unroll
+        for (int j = 0; j < std::decay_t<decltype(op)>::kLoads; ++j) op.load(st, (ZERO_LDS char*)to, j);
+    };
+    // Share g of 4 of the loads of the first two steps; step 1's a comes last.
+    auto first_loads = [&](int g) -> void {
+        if (g == 0) load(oa, 0, s0);
+        else if (g == 1) load(ob, 0, s1);
+        else if (g == 2) load(ob, 1, s3);
+        else load(oa, 1, s2);
+    };
+    auto begin = [&](int id) -> void {
+        w = place(id);
+        oa.setup(q.a + (LA == kRows ? w.m0 * q.lda + w.k_lo * 2 : w.k_lo * q.lda + w.m0 * 2), q.lda, q.m - w.m0,
+                 w.m0, w.k_lo, w.k);
+        ob.setup(q.b + (LB == kRows ? w.n0 * q.ldb + w.k_lo * 2 : w.k_lo * q.ldb + w.n0 * 2), q.ldb, q.n - w.n0,
+                 w.n0, w.k_lo, w.k);
+    };
+    // of the 8 consecutive m that a lane holds after pair()
+    [[maybe_unused]] const int pair_m = ((lane >> 4) & 1) * 16 + (lane >> 5) * 8;
     f32x4 acc[FM][FN];
-    #pragma unroll
-    for (int i = 0; i < FM; ++i)
-        #pragma unroll
-        for (int j = 0; j < FN; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto load = [&](char* sha, char* shb, int step) {
-        const int left = k_hi - k_lo - step * kTileK;
-        oa.load(pa + step * sa, LA == kRows ? (k_lo + step * kTileK) * 2 : m0 * 2, left, (ZERO_LDS char*)sha);
-        ob.load(pb + step * sb, LB == kRows ? (k_lo + step * kTileK) * 2 : n0 * 2, left, (ZERO_LDS char*)shb);
+    struct Frags {
+        s16x8 a[FM], b[FN];
     };
-    auto multiply = [&](const char* sha, const char* shb) {
-        #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            // both halves' fragments at once would not fit the registers
+    const uint32_t at_a = OpA::first(wm), at_b = OpB::first(wn);
+    auto read = [&](Frags& f, const char* sha, const char* shb, uint32_t fa, uint32_t fb, int h, int r) {
+        if (r < FN) f.b[r] = OpB::fragment((const ZERO_LDS char*)shb, fb, r, h);
+        else f.a[r - FN] = OpA::fragment((const ZERO_LDS char*)sha, fa, r - FN, h);
+    };
+    // The products of one half of a step's k.  With one wave a SIMD the matrix
+    // core idles wherever two other instructions stand in a row, so the reads
+    // of the next half's fragments and the loads of a later step go one by one
+    // between them, over the first three quarters: the last reads have arrived
+    // when the next half begins.
+    auto half = [&](const Frags& use, Frags& fill, const char* sha, const char* shb, int h, const auto& op, int t,
+                    char* to) __attribute__((always_inline)) -> void {
+        constexpr int kItems = FM + FN + std::decay_t<decltype(op)>::kLoads;
+        constexpr int kLoads = std::decay_t<decltype(op)>::kLoads;
+        constexpr int kSpan = FM * FN * 3 / 4 > 0 ? FM * FN * 3 / 4 : 1;
+        // hidden, or every address of every slot takes a register of its own
+        uint32_t fa = at_a, fb = at_b;
+        asm volatile("" : "+v"(fa), "+v"(fb));
+        const auto st = op.step(t, w.k);
+        each<FM * FN>([&](auto slot) __attribute__((always_inline)) -> void {
+            constexpr int s = decltype(slot)::value;
             __builtin_amdgcn_sched_barrier(0);
-            s16x8 fa[FM], fb[FN];
-            #pragma unroll
-            for (int i = 0; i < FM; ++i) fa[i] = OpA::fragment((const ZERO_LDS char*)sha, wm + i * 16, h);
-            #pragma unroll
-            for (int j = 0; j < FN; ++j) fb[j] = OpB::fragment((const ZERO_LDS char*)shb, wn + j * 16, h);
-            #pragma unroll
-            for (int i = 0; i < FM; ++i)
-                #pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = mfma<DT>(fa[i], fb[j], acc[i][j]);
-        }
+            mfma<DT>(acc[s / FN][s % FN], use.a[s / FN], use.b[s % FN]);
+            constexpr int from = s < kSpan ? s * kItems / kSpan : kItems;
+            constexpr int to_x = s < kSpan ? (s + 1) * kItems / kSpan : kItems;
+            each<to_x - from>([&](auto item) __attribute__((always_inline)) -> void {
+                constexpr int x = from + decltype(item)::value, l = x * kLoads / kItems;
+                if constexpr ((x + 1) * kLoads / kItems > l) op.load(st, (ZERO_LDS char*)to, l);
+                else read(fill, sha, shb, fa, fb, h, x - l);
+            });
+        });
+        __builtin_amdgcn_sched_barrier(0);
     };
-    // a stage is read only after its loads arrived in every wave, and loaded
-    // again only after every wave has read it
-    auto turn = [] {
-        __builtin_amdgcn_s_waitcnt(0x0f70);            // vmcnt(0): the loads into LDS
-        __syncthreads();
+    Frags f0, f1;
+    // Step t lies in slots a and b, step t + 1 in a1 and b1.  Slot a2 was
+    // step t - 1's b: every wave's reads of it ended before the turn of step
+    // t - 1.  The reads of a end before the turn here, after which it takes
+    // step t + 2's b.
+    auto step = [&](int t, char* a, char* b, char* a1, char* b1, char* a2) __attribute__((always_inline)) {
+        half(f0, f1, a, b, 1, oa, t + 2, a2);
+        // all but the loads of a2 have arrived, in every wave
+        __builtin_amdgcn_s_waitcnt(0x0070 | OpA::kLoads);
+        __builtin_amdgcn_s_barrier();
+        half(f1, f0, a1, b1, 0, ob, t + 2, a);
     };
-    if (steps > 0) load(a0, b0, 0);
-    int s = 0;
-    for (; s + 2 <= steps; s += 2) {
-        turn();
-        load(a1, b1, s + 1);
-        multiply(a0, b0);
-        turn();
-        if (s + 2 < steps) load(a0, b0, s + 2);
-        multiply(a1, b1);
-    }
-    if (s < steps) {
-        turn();
-        multiply(a0, b0);
-    }
-
+    static_assert(OpA::kLoads < 16, "the wait's low bits");
     // acc[i][j][e] is C at n = n0 + wn + 16 j + lane % 16,
     // m = m0 + wm + 16 i + 4 (lane / 16) + e
-    const int lane = threadIdx.x & 63, nl = lane & 15, ml = (lane >> 4) * 4;
-    if constexpr (E == kLse) {
-        const int slot = q.slot0 + tm * WM + wave % WM;
-        #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int n = n0 + wn + j * 16 + nl;
-            const bool live = n < q.n;
-            // position of the target among this lane's m, if it is there
-            const int64_t tgt = live ? q.target[n] : -1;
-            const int64_t at = tgt - q.first_m - m0 - wm - ml;
-            float top = -__builtin_inff(), hit = 0.0f;
-            bool found = false;
+    // The epilogues' code is kept short: it runs once a tile, and straight-line
+    // code past the instruction cache costs more to fetch than to run.
+    auto epilogue = [&](int tm, int m0, int n0, int slice, const int64_t (&target)[FN], const float (&lse)[FN],
+                        bool more) __attribute__((always_inline)) -> void {
+        // the next tile's first loads, a share with each of the first four columns
+        auto columns = [&](auto column) __attribute__((always_inline)) -> void {
+            each<FN>([&](auto index) __attribute__((always_inline)) -> void {
+                constexpr int j = decltype(index)::value, kShares = FN < 4 ? FN : 4;
+                __builtin_amdgcn_sched_barrier(0);
+                if (more) {
+                    each<4>([&](auto share) __attribute__((always_inline)) -> void {
+                        constexpr int g = decltype(share)::value;
+                        if constexpr (g * kShares / 4 == j) first_loads(g);
+                    });
+                }
+                column(index);
+            });
+        };
+        [[maybe_unused]] const int end = q.m - (m0 + wm + ml);   // the lane's elements 16 i + e below it exist
+        // the target's place from this lane's first m on
+        [[maybe_unused]] int at[FN];
+        if constexpr (E == kLse || E == kProb) {
             #pragma unroll
-            for (int i = 0; i < FM; ++i)
+            for (int j = 0; j < FN; ++j)
+                at[j] = target[j] >= 0 && target[j] < q.vocab
+                            ? static_cast<int>(target[j]) - q.first_m - (m0 + wm + ml) : kNotKept;
+        }
+        [[maybe_unused]] auto split = [&](auto column) __attribute__((always_inline)) -> void {
+            if (m0 + BM > q.m)
+                columns([&](auto index) __attribute__((always_inline)) -> void { column(std::true_type{}, index); });
+            else
+                columns([&](auto index) __attribute__((always_inline)) -> void { column(std::false_type{}, index); });
+        };
+        // kLse, kProb: an element, -inf beyond the last m where a tile has such
+        auto logit = [&](auto edge, int i, int j, int e) __attribute__((always_inline)) -> float {
+            const float x = taken(acc[i][j], e);
+            return !decltype(edge)::value || i * 16 + e < end ? x : -__builtin_inff();
+        };
+        if constexpr (E == kLse) {
+            const int slot = q.slot0 + tm * WM + wave % WM;
+            auto column = [&](auto edge, auto index) __attribute__((always_inline)) -> void {
+                constexpr int j = decltype(index)::value;
+                const int n = n0 + wn + j * 16 + nl;
+                f32x4 x[FM];
                 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if (m0 + wm + i * 16 + ml + e >= q.m) acc[i][j][e] = -__builtin_inff();
-                    top = fmaxf(top, acc[i][j][e]);
-                    if (at == i * 16 + e) {
-                        hit = acc[i][j][e];
-                        found = true;
+                for (int i = 0; i < FM; ++i)
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) x[i][e] = logit(edge, i, j, e);
+                float top = max3(x[0][0], x[0][1], max3(x[0][2], x[0][3], x[0][3]));
+                #pragma unroll
+                for (int i = 1; i < FM; ++i) top = max3(x[i][0], x[i][1], max3(x[i][2], x[i][3], top));
+                top = fmaxf(other_row(top).x, other_row(top).y);
+                top = fmaxf(other_half(top).x, other_half(top).y);
+                // exp(x - top) as 2^(x log2 e - c) 2^(c - top log2 e)
+                const float base = infinite(top) ? 0.0f : top;
+                const float c = base * kLog2e, rest = __builtin_fmaf(base, -kLog2e, c);
+                f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f}, y[FM];
+                #pragma unroll
+                for (int i = 0; i <= FM; ++i) {
+                    // a row's sums go with the next row's exponentials
+                    __builtin_amdgcn_sched_barrier(0);
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (i < FM) y[i][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[i][e], kLog2e, -c));
+                        if (i > 0) part[e] += y[i - 1][e];
                     }
                 }
-            top = fmaxf(top, __shfl_xor(top, 16, 64));
-            top = fmaxf(top, __shfl_xor(top, 32, 64));
-            const float base = infinite(top) ? 0.0f : top;
-            float sum = 0.0f;
-            #pragma unroll
-            for (int i = 0; i < FM; ++i)
-                #pragma unroll
-                for (int e = 0; e < 4; ++e) sum += __expf(acc[i][j][e] - base);
-            sum += __shfl_xor(sum, 16, 64);
-            sum += __shfl_xor(sum, 32, 64);
-            if (live && lane < 16)
-                reinterpret_cast<f32x2*>(q.partial)[static_cast<int64_t>(slot) * q.n + n] = f32x2{top, sum};
-            if (found && tgt < q.vocab) q.target_logit[n] = hit;
-        }
-    } else if constexpr (E == kProb) {
-        #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int n = n0 + wn + j * 16 + nl;
-            if (n >= q.n) continue;
-            const int64_t tgt = q.target[n];
-            const bool kept = tgt >= 0 && tgt < q.vocab;
-            const float lse = q.lse[n];
-            const int64_t at = tgt - q.first_m - m0 - wm - ml;
-            unsigned short* row = reinterpret_cast<unsigned short*>(q.c) + n * q.ldc + m0 + wm + ml;
-            #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                float p[4];
-                #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    p[e] = __expf(acc[i][j][e] - lse) - (at == i * 16 + e ? 1.0f : 0.0f);
-                    p[e] = kept && m0 + wm + i * 16 + ml + e < q.m ? p[e] * q.scale : 0.0f;
+                float sum = ((part[0] + part[1]) + (part[2] + part[3])) * __builtin_amdgcn_exp2f(rest);
+                sum = other_row(sum).x + other_row(sum).y;
+                sum = other_half(sum).x + other_half(sum).y;
+                if (n < q.n && lane < 16)
+                    reinterpret_cast<f32x2*>(q.partial)[static_cast<int64_t>(slot) * q.n + n] = f32x2{top, sum};
+                const bool hit = n < q.n && here<FM>(at[j]);
+                if (__builtin_amdgcn_ballot_w64(hit) != 0) {
+                    const float v = pick(x, at[j]);
+                    if (hit) q.target_logit[n] = v;
                 }
-                u32x2 o;
-                o.x = pack2<DT>(p[0], p[1]);
-                o.y = pack2<DT>(p[2], p[3]);
-                *reinterpret_cast<u32x2*>(row + i * 16) = o;
-            }
-        }
-    } else if constexpr (E == kSlab) {
-        float* c = reinterpret_cast<float*>(q.c) + static_cast<int64_t>(blockIdx.y) * q.slab;
-        #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int n = n0 + wn + j * 16 + nl;
-            if (n >= q.n) continue;
-            #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int m = m0 + wm + i * 16 + ml;
-                if (m >= q.m) continue;                   // q.m and ldc are whole quads
-                f32x4* at = reinterpret_cast<f32x4*>(c + n * q.ldc + m);
-                f32x4 x = acc[i][j];
-                if (q.add) {
-                    const f32x4 y = *at;
-                    #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = y[e] + x[e];
-                }
-                *at = x;
-            }
-        }
-    } else {
-        const float f = q.scale * q.result->inv_count;
-        typedef u32x2 quad __attribute__((aligned(2)));
-        #pragma unroll
-        for (int j = 0; j < FN; ++j) {
-            const int n = n0 + wn + j * 16 + nl;
-            if (n >= q.n) continue;
-            unsigned short* row = reinterpret_cast<unsigned short*>(q.c) + n * q.ldc;
-            #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                const int m = m0 + wm + i * 16 + ml;
-                const f32x4 x = acc[i][j];
-                if (m + 4 <= q.valid_m) {
-                    u32x2 o;
-                    o.x = pack2<DT>(x[0] * f, x[1] * f);
-                    o.y = pack2<DT>(x[2] * f, x[3] * f);
-                    *reinterpret_cast<quad*>(row + m) = o;
-                } else {
+            };
+            split(column);
+        } else if constexpr (E == kProb) {
+            const float bias = q.scale > 1.0f ? 15.0f : 0.0f;      // log2 of the scale
+            auto column = [&](auto edge, auto index) __attribute__((always_inline)) -> void {
+                constexpr int j = decltype(index)::value;
+                const int n = n0 + wn + j * 16 + nl;
+                f32x4 p[FM];
+                #pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    __builtin_amdgcn_sched_barrier(0);
                     #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (m + e < q.valid_m) row[m + e] = pack1<DT>(x[e] * f);
+                        p[i][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(logit(edge, i, j, e) - lse[j], kLog2e, bias));
                 }
+                const bool kept = at[j] != kNotKept, hit = n < q.n && here<FM>(at[j]);
+                if (__builtin_amdgcn_ballot_w64(hit) != 0) {
+                    #pragma unroll
+                    for (int i = 0; i < FM; ++i)
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e) p[i][e] -= at[j] == i * 16 + e ? q.scale : 0.0f;
+                }
+                unsigned short* row = reinterpret_cast<unsigned short*>(q.c) + n * q.ldc + m0 + wm;
+                #pragma unroll
+                for (int i = 0; i < FM; i += 2) {
+                    const u32x4 o = pair<DT>(p[i], p[i + 1], 1.0f);
+                    if (n < q.n) *reinterpret_cast<u32x4*>(row + i * 16 + pair_m) = kept ? o : u32x4{0u, 0u, 0u, 0u};
+                }
+            };
+            split(column);
+        } else if constexpr (E == kSlab) {
+            float* c = reinterpret_cast<float*>(q.c) + static_cast<int64_t>(slice) * q.slab;
+            columns([&](auto index) __attribute__((always_inline)) -> void {
+                constexpr int j = decltype(index)::value;
+                const int n = n0 + wn + j * 16 + nl;
+                f32x4* row = reinterpret_cast<f32x4*>(c + n * q.ldc + m0 + wm + ml);
+                f32x4 y[FM];
+                #pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    y[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    // q.m and ldc are whole quads
+                    if (q.add && n < q.n && i * 16 < end) y[i] = row[i * 4];
+                }
+                #pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    f32x4 x = taken(acc[i][j]);
+                    #pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = y[i][e] + x[e];
+                    if (n < q.n && i * 16 < end) row[i * 4] = x;
+                }
+            });
+        } else {
+            const float f = q.scale * q.result->inv_count;
+            typedef u32x4 eight __attribute__((aligned(2)));
+            columns([&](auto index) __attribute__((always_inline)) -> void {
+                constexpr int j = decltype(index)::value;
+                const int n = n0 + wn + j * 16 + nl;
+                unsigned short* row = reinterpret_cast<unsigned short*>(q.c) + n * q.ldc;
+                #pragma unroll
+                for (int i = 0; i < FM; i += 2) {
+                    const u32x4 o = pair<DT>(taken(acc[i][j]), taken(acc[i + 1][j]), f);
+                    const int m = m0 + wm + i * 16 + pair_m;
+                    if (n >= q.n || m >= q.valid_m) continue;
+                    if (m + 8 <= q.valid_m) {
+                        *reinterpret_cast<eight*>(row + m) = o;
+                    } else {
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (m + e < q.valid_m) row[m + e] = static_cast<unsigned short>(o[e / 2] >> (16 * (e % 2)));
+                    }
+                }
+            });
+        }
+    };
+
+    begin(blockIdx.x);
+    #pragma unroll
+    for (int g = 0; g < 4; ++g) first_loads(g);
+    for (int id = blockIdx.x;;) {
+        #pragma unroll
+        for (int i = 0; i < FM; ++i)
+            #pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                asm volatile("" : "+a"(acc[i][j]));        // written here, well before the first product
+            }
+        // The loads of step 1's a, which came last, may still be under way (so
+        // may stores of the last tile's epilogue, which came after them).
+        __builtin_amdgcn_s_waitcnt(0x0070 | OpA::kLoads);
+        __builtin_amdgcn_s_barrier();
+        // what the epilogue needs of each token is here long before it
+        [[maybe_unused]] int64_t target[FN];
+        [[maybe_unused]] float lse[FN];
+        if constexpr (E == kLse || E == kProb) {
+            #pragma unroll
+            for (int j = 0; j < FN; ++j) {
+                const int n = w.n0 + wn + j * 16 + nl;
+                target[j] = q.target[n < q.n ? n : q.n - 1];
+                if constexpr (E == kProb) lse[j] = q.lse[n < q.n ? n : q.n - 1];
             }
         }
+        #pragma unroll
+        for (int x = 0; x < FM + FN; ++x) read(f0, s0, s1, at_a, at_b, 0, x);
+        const int steps = (w.k + kTileK - 1) / kTileK;
+        for (int t = 0; t < steps; t += 5) {
+            step(t, s0, s1, s2, s3, s4);
+            if (t + 1 < steps) step(t + 1, s2, s3, s4, s0, s1);
+            if (t + 2 < steps) step(t + 2, s4, s0, s1, s2, s3);
+            if (t + 3 < steps) step(t + 3, s1, s2, s3, s4, s0);
+            if (t + 4 < steps) step(t + 4, s3, s4, s0, s1, s2);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0070);                // no load outlives the tile
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("s_nop 15\n\ts_nop 15");              // the last products' results, which the compiler does not time
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        const int tm = w.tm, m0 = w.m0, n0 = w.n0, slice = w.slice;
+        id += gridDim.x;
+        if (id < total) begin(id);
+        epilogue(tm, m0, n0, slice, target, lse, id < total);
+        if (id >= total) break;
     }
 }
 
@@ -563,9 +787,12 @@ template <int DT, Layout LA, Layout LB, Epilogue E, int BM, int BN, int WM, int 
 void launch_tiles(Product q, int slices, hipStream_t st) {
     q.tiles_m = (q.m + BM - 1) / BM;
     q.tiles_n = (q.n + BN - 1) / BN;
+    q.slices = slices;
+    // as many blocks as the CUs' LDS holds at once
+    constexpr int kBlocks = kCus * (kLdsBytes / (5 * (BM > BN ? BM : BN) * kTileK * 2));
+    const int total = q.tiles_m * q.tiles_n * slices;
     hipLaunchKernelGGL((product_kernel<DT, LA, LB, E, BM, BN, WM, WN>),
-                       dim3(static_cast<unsigned>(q.tiles_m * q.tiles_n), static_cast<unsigned>(slices)),
-                       dim3(WM * WN * 64), 0, st, q);
+                       dim3(static_cast<unsigned>(total < kBlocks ? total : kBlocks)), dim3(WM * WN * 64), 0, st, q);
 }
 
 int64_t tiles_of(const Product& q, int64_t bm, int64_t bn) { return up(q.m, bm) / bm * (up(q.n, bn) / bn); }
@@ -573,7 +800,7 @@ int64_t tiles_of(const Product& q, int64_t bm, int64_t bn) { return up(q.m, bm) 
 // Returns the wave rows of a tile and their extent in m (for kLse's slots).
 template <int DT, Layout LA, Layout LB, Epilogue E>
 void launch_product(const Product& q, int slices, hipStream_t st) {
-    if (tiles_of(q, 256, 256) * slices >= 192) launch_tiles<DT, LA, LB, E, 256, 256, 2, 4>(q, slices, st);
+    if (tiles_of(q, 256, 256) * slices >= 192) launch_tiles<DT, LA, LB, E, 256, 256, 2, 2>(q, slices, st);
     else launch_tiles<DT, LA, LB, E, 128, 128, 2, 2>(q, slices, st);
 }
 
@@ -636,7 +863,7 @@ int forward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
         q.target_logit = hit;
         q.vocab = static_cast<int32_t>(a->vocab);
         if (tiles_of(q, 256, 256) >= 192) {
-            launch_tiles<DT, kRows, kRows, kLse, 256, 256, 2, 4>(q, 1, st);
+            launch_tiles<DT, kRows, kRows, kLse, 256, 256, 2, 2>(q, 1, st);
             slots += static_cast<int>(up(rows, 256) / 256 * 2);
         } else if (a->tokens <= kFewTokens) {
             launch_tiles<DT, kRows, kRows, kLse, 64, 16, 4, 1>(q, 1, st);
