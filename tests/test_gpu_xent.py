@@ -214,3 +214,40 @@ def test_captured_and_on_a_side_stream():
         for name in ("d_dx", "d_dw"):
             assert torch.equal(getattr(c, name), getattr(e, name)), (rep, name)
         assert torch.equal(c.args.lse, e.args.lse) and torch.equal(c.args.result, e.args.result)
+
+
+# several pieces of the vocabulary: of 256 MB of P, and of 128 MB where w's rows are repacked
+@pytest.mark.parametrize("size", [(16384, 64, 8500), (16384, 61, 4200)], ids=lambda s: "x".join(map(str, s)))
+def test_pieces(size):
+    say("%s" % (size,))
+    c = Call(*size, torch.bfloat16, ignored=0.1)
+    c.run()
+    x, w = c.x.cuda(), c.w.cuda()
+    r = train_ref.xent(x, w, c.args.target)
+    b = train_ref.xent_bounds(r, x, w, c.dtype)
+    for name in ("loss", "lse", "dx", "dw"):
+        got = getattr(c, "d_" + name) if name in ("dx", "dw") else getattr(c.args, name)
+        assert bool(((got.double() - r[name]).abs() <= b[name]).all()), name
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("size", [(5, 64, 300), (300, 72, 515), (2100, 64, 700)], ids=lambda s: "x".join(map(str, s)))
+def test_masked_rows_reach_no_sum(size, bad):
+    # rows of x without a target hold NaN or infinities: the others' loss and
+    # all of dx and dw are those of the batch without these rows
+    c = Call(*size, torch.bfloat16, ignored=0.0, seed=3)
+    masked = torch.arange(size[0]) % 3 == 1
+    masked[-1] = True
+    c.target[masked] = -100
+    c.args.target.copy_(c.target)
+    c.d_x[masked.cuda()] = bad
+    c.run()
+    x = c.x.clone()
+    x[masked] = 0.0
+    r = train_ref.xent(x, c.w, c.target)
+    b = train_ref.xent_bounds(r, x, c.w, c.dtype)
+    for name in ("dx", "dw"):
+        assert bool(((getattr(c, "d_" + name).cpu().double() - r[name]).abs() <= b[name]).all()), name
+    loss = c.args.loss.cpu().double()
+    assert bool(((loss - r["loss"]).abs() <= b["loss"]).all()) and c.result().count == int((~masked).sum())
+    assert not bool(c.d_dx[masked.cuda()].any())

@@ -52,7 +52,7 @@ struct Product {
     const char* b;
     int64_t lda, ldb;         // bytes from row to row
     int32_t m, n, k;          // extents; along a kCols operand's m or n whole 16 bytes are read
-    int32_t tiles_m, tiles_n;
+    int32_t tiles_m;
     int32_t slices, slice;    // slices of k, and k of one: a multiple of kTileK
     // epilogues
     char* c;                  // P, slabs or gradient
@@ -69,6 +69,7 @@ struct Product {
     const zero_xent_result_t* result;   // kGrad: inv_count
     float scale;              // kProb: applied before rounding; kGrad: undone, times grad_scale
     int32_t vocab;
+    const int32_t* kept;      // the backward: how many tokens there are; n or k is their most
 };
 
 // f(0), f(1) .. f(N - 1), each number a constant.
@@ -272,7 +273,11 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
 
     // The grid is what the chip holds at once; a block walks the tiles of all
     // slices.
-    const int tiles = q.tiles_m * q.tiles_n, total = tiles * q.slices;
+    constexpr bool kTokensAreK = LB == kCols, kTokensAreN = E == kProb || (E == kSlab && !kTokensAreK);
+    const int size_n = kTokensAreN ? *q.kept : q.n, size_k = kTokensAreK ? *q.kept : q.k;
+    const int tiles_n = (size_n + BN - 1) / BN;
+    const int tiles = q.tiles_m * tiles_n, total = tiles * q.slices;
+    if (static_cast<int>(blockIdx.x) >= total) return;
     struct Place {
         int tm, m0, n0, slice, k_lo, k;                    // k: this slice's
     };
@@ -287,13 +292,13 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
         id = x * per + (x < extra ? x : extra) + i;
         constexpr int kStrip = 4;
         const int strip = id / (kStrip * q.tiles_m);
-        const int width = q.tiles_n - strip * kStrip < kStrip ? q.tiles_n - strip * kStrip : kStrip;
+        const int width = tiles_n - strip * kStrip < kStrip ? tiles_n - strip * kStrip : kStrip;
         const int in_strip = id - strip * kStrip * q.tiles_m;
         w.tm = in_strip / width;
         w.m0 = w.tm * BM;
         w.n0 = (strip * kStrip + in_strip % width) * BN;
         w.k_lo = w.slice * q.slice;
-        w.k = (q.k < w.k_lo + q.slice ? q.k : w.k_lo + q.slice) - w.k_lo;
+        w.k = (size_k < w.k_lo + q.slice ? size_k : w.k_lo + q.slice) - w.k_lo;
         w.k = w.k > 0 ? w.k : 0;
         return w;
     };
@@ -321,7 +326,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
         w = place(id);
         oa.setup(q.a + (LA == kRows ? w.m0 * q.lda + w.k_lo * 2 : w.k_lo * q.lda + w.m0 * 2), q.lda, q.m - w.m0,
                  w.m0, w.k_lo, w.k);
-        ob.setup(q.b + (LB == kRows ? w.n0 * q.ldb + w.k_lo * 2 : w.k_lo * q.ldb + w.n0 * 2), q.ldb, q.n - w.n0,
+        ob.setup(q.b + (LB == kRows ? w.n0 * q.ldb + w.k_lo * 2 : w.k_lo * q.ldb + w.n0 * 2), q.ldb, size_n - w.n0,
                  w.n0, w.k_lo, w.k);
     };
     // of the 8 consecutive m that a lane holds after pair()
@@ -449,9 +454,9 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 float sum = ((part[0] + part[1]) + (part[2] + part[3])) * __builtin_amdgcn_exp2f(rest);
                 sum = other_row(sum).x + other_row(sum).y;
                 sum = other_half(sum).x + other_half(sum).y;
-                if (n < q.n && lane < 16)
-                    reinterpret_cast<f32x2*>(q.partial)[static_cast<int64_t>(slot) * q.n + n] = f32x2{top, sum};
-                const bool hit = n < q.n && here<FM>(at[j]);
+                if (n < size_n && lane < 16)
+                    reinterpret_cast<f32x2*>(q.partial)[static_cast<int64_t>(slot) * size_n + n] = f32x2{top, sum};
+                const bool hit = n < size_n && here<FM>(at[j]);
                 if (__builtin_amdgcn_ballot_w64(hit) != 0) {
                     const float v = pick(x, at[j]);
                     if (hit) q.target_logit[n] = v;
@@ -471,7 +476,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                     for (int e = 0; e < 4; ++e)
                         p[i][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(logit(edge, i, j, e) - lse[j], kLog2e, bias));
                 }
-                const bool kept = at[j] != kNotKept, hit = n < q.n && here<FM>(at[j]);
+                const bool kept = at[j] != kNotKept, hit = n < size_n && here<FM>(at[j]);
                 if (__builtin_amdgcn_ballot_w64(hit) != 0) {
                     #pragma unroll
                     for (int i = 0; i < FM; ++i)
@@ -482,7 +487,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 #pragma unroll
                 for (int i = 0; i < FM; i += 2) {
                     const u32x4 o = pair<DT>(p[i], p[i + 1], 1.0f);
-                    if (n < q.n) *reinterpret_cast<u32x4*>(row + i * 16 + pair_m) = kept ? o : u32x4{0u, 0u, 0u, 0u};
+                    if (n < size_n) *reinterpret_cast<u32x4*>(row + i * 16 + pair_m) = kept ? o : u32x4{0u, 0u, 0u, 0u};
                 }
             };
             split(column);
@@ -497,14 +502,14 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 for (int i = 0; i < FM; ++i) {
                     y[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                     // q.m and ldc are whole quads
-                    if (q.add && n < q.n && i * 16 < end) y[i] = row[i * 4];
+                    if (q.add && n < size_n && i * 16 < end) y[i] = row[i * 4];
                 }
                 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
                     f32x4 x = taken(acc[i][j]);
                     #pragma unroll
                     for (int e = 0; e < 4; ++e) x[e] = y[i][e] + x[e];
-                    if (n < q.n && i * 16 < end) row[i * 4] = x;
+                    if (n < size_n && i * 16 < end) row[i * 4] = x;
                 }
             });
         } else {
@@ -518,7 +523,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 for (int i = 0; i < FM; i += 2) {
                     const u32x4 o = pair<DT>(taken(acc[i][j]), taken(acc[i + 1][j]), f);
                     const int m = m0 + wm + i * 16 + pair_m;
-                    if (n >= q.n || m >= q.valid_m) continue;
+                    if (n >= size_n || m >= q.valid_m) continue;
                     if (m + 8 <= q.valid_m) {
                         *reinterpret_cast<eight*>(row + m) = o;
                     } else {
@@ -553,8 +558,8 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
             #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 const int n = w.n0 + wn + j * 16 + nl;
-                target[j] = q.target[n < q.n ? n : q.n - 1];
-                if constexpr (E == kProb) lse[j] = q.lse[n < q.n ? n : q.n - 1];
+                target[j] = q.target[n < size_n ? n : size_n - 1];
+                if constexpr (E == kProb) lse[j] = q.lse[n < size_n ? n : size_n - 1];
             }
         }
         #pragma unroll
@@ -656,11 +661,13 @@ __global__ __launch_bounds__(1024) void xent_mean_kernel(const float* __restrict
     }
 }
 
-// The slabs' sum times the factor, 16 bits; slabs in order.
+// The slabs' sum times the factor, 16 bits; slabs in order.  With `rank` a
+// row's sum is in row rank[r], and 0 where that is negative.
 template <int DT>
 __global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__ slabs, int n_slabs, int64_t slab,
                                                        int64_t rows, int64_t dim, int64_t ld,
                                                        const zero_xent_result_t* __restrict__ result, float scale,
+                                                       const int32_t* __restrict__ rank,
                                                        unsigned short* __restrict__ out, int64_t out_stride) {
     typedef u32x2 quad __attribute__((aligned(2)));
     const int64_t quads = ld / 4;
@@ -669,8 +676,9 @@ __global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__
         const int64_t r = at / quads, d = (at - r * quads) * 4;
         if (d >= dim) continue;
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < n_slabs; ++s) {
-            const f32x4 y = *reinterpret_cast<const f32x4*>(slabs + s * slab + r * ld + d);
+        const int64_t from = rank ? rank[r] : r;
+        for (int s = 0; s < (from < 0 ? 0 : n_slabs); ++s) {
+            const f32x4 y = *reinterpret_cast<const f32x4*>(slabs + s * slab + from * ld + d);
             #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] += y[e];
         }
@@ -689,30 +697,86 @@ __global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__
     }
 }
 
+// Elements [d, d + 8) of a row of any alignment, zeros past dim.
+__device__ __forceinline__ u32x4 row_piece(const unsigned short* __restrict__ s, int64_t d, int64_t dim) {
+    typedef u32x4 piece __attribute__((aligned(2)));
+    if (d + 8 <= dim) return *reinterpret_cast<const piece*>(s + d);
+    unsigned w[4] = {0u, 0u, 0u, 0u};
+    #pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (d + e < dim) w[e / 2] |= static_cast<unsigned>(s[d + e]) << (16 * (e % 2));
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
 // Rows of any stride and alignment into rows of ld elements (a multiple of
 // 64), zeros past dim: what the products read where the caller's rows are
 // not whole 16-byte pieces.
 __global__ __launch_bounds__(256) void repack_kernel(const unsigned short* __restrict__ src, int64_t stride,
                                                      int64_t rows, int64_t dim, int64_t ld,
                                                      unsigned short* __restrict__ dst) {
-    typedef u32x4 piece __attribute__((aligned(2)));
     const int64_t pieces = ld / 8;
     for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < rows * pieces;
          at += static_cast<int64_t>(gridDim.x) * 256) {
         const int64_t r = at / pieces, d = (at - r * pieces) * 8;
-        const unsigned short* s = src + r * stride + d;
-        u32x4 o = {0u, 0u, 0u, 0u};
-        if (d + 8 <= dim) {
-            o = *reinterpret_cast<const piece*>(s);
-        } else {
-            unsigned w[4] = {0u, 0u, 0u, 0u};
-            #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (d + e < dim) w[e / 2] |= static_cast<unsigned>(s[e]) << (16 * (e % 2));
-            o = u32x4{w[0], w[1], w[2], w[3]};
-        }
-        *reinterpret_cast<u32x4*>(dst + r * ld + d) = o;
+        *reinterpret_cast<u32x4*>(dst + r * ld + d) = row_piece(src + r * stride, d, dim);
     }
+}
+
+// The tokens that have a target, one after another: their rows of x (as
+// repack_kernel lays them), targets and lse, how many they are, and every
+// token's place among them (-1: none).  The gradient's products then run
+// over these alone: a masked token costs nothing there, and what its row
+// holds, be it NaN, reaches no sum.  A block places `chunk` tokens and
+// counts those before them by itself.
+__global__ __launch_bounds__(256) void gather_kernel(const unsigned short* __restrict__ x, int64_t stride, int64_t dim,
+                                                     int64_t ld, const int64_t* __restrict__ target,
+                                                     const float* __restrict__ lse, int64_t vocab, int tokens,
+                                                     int chunk, unsigned short* __restrict__ x_out,
+                                                     int64_t* __restrict__ target_out, float* __restrict__ lse_out,
+                                                     int32_t* __restrict__ rank, int32_t* __restrict__ kept) {
+    __shared__ int s_count[4], s_rank[256];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x / 64;
+    const int first = blockIdx.x * chunk, last = first + chunk < tokens ? first + chunk : tokens;
+    auto has = [&](int i, int end) { return i < end && target[i] >= 0 && target[i] < vocab; };
+    // the four waves' counts as one; every thread calls it
+    auto join = [&](int mine, int* before) {
+        __syncthreads();
+        if (lane == 0) s_count[wave] = mine;
+        __syncthreads();
+        int all = 0;
+        *before = 0;
+        for (int k = 0; k < 4; ++k) {
+            *before += k < wave ? s_count[k] : 0;
+            all += s_count[k];
+        }
+        return all;
+    };
+    int mine = 0, before = 0;
+    for (int i = 0; i < first; i += 256) mine += __popcll(__builtin_amdgcn_ballot_w64(has(i + threadIdx.x, first)));
+    int base = join(mine, &before);
+    for (int b = first; b < last; b += 256) {
+        const int i = b + threadIdx.x;
+        const bool here = has(i, last);
+        const uint64_t mask = __builtin_amdgcn_ballot_w64(here);
+        const int all = join(__popcll(mask), &before);
+        const int at = base + before + __popcll(mask & ((uint64_t(1) << lane) - 1));
+        base += all;
+        s_rank[threadIdx.x] = here ? at : -1;
+        if (i < last) rank[i] = here ? at : -1;
+        if (here) {
+            target_out[at] = target[i];
+            lse_out[at] = lse[i];
+        }
+        __syncthreads();
+        const int n = last - b < 256 ? last - b : 256;
+        for (int r = wave; r < n; r += 4) {
+            const int64_t to = s_rank[r];
+            if (to < 0) continue;
+            for (int64_t d = lane * 8; d < ld; d += 512)
+                *reinterpret_cast<u32x4*>(x_out + to * ld + d) = row_piece(x + (b + r) * stride, d, dim);
+        }
+    }
+    if (last == tokens && threadIdx.x == 0) *kept = base;
 }
 
 // No token: nothing to add up, dw is zero.
@@ -731,28 +795,28 @@ int launch_error(const char* what) {
 
 constexpr int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
-// How a problem is cut.  Everything depends on the three sizes only.
+// How a problem is cut.  Everything depends on the three sizes only, and on
+// whether w is repacked.
 struct Cut {
     int64_t dim_pad;          // row of a repacked operand and of a slab
     int64_t piece;            // vocabulary of one piece of the backward, a multiple of 256
     int64_t slots;            // most partials per token of the forward
     int32_t dx_slices, dw_slices;
-    size_t x_bytes, w_bytes, p_bytes, slab_bytes, part_bytes;
+    size_t x_bytes, row_bytes, w_bytes, p_bytes, slab_bytes, part_bytes;
     size_t total;
 };
 
 constexpr int64_t kMaxTokens = int64_t(1) << 20, kMaxDim = int64_t(1) << 20, kMaxVocab = int64_t(1) << 24;
 constexpr int64_t kFewTokens = 16;            // one tile of tokens in the forward
-constexpr int64_t kPBytes = int64_t(64) << 20, kWBytes = int64_t(256) << 20;
+// Of P, and of a piece of w repacked.  A larger piece costs room and saves
+// dx's slab a trip: at 4096 tokens x 4096 x 128000, @PIECES@
+constexpr int64_t kPBytes = int64_t(256) << 20, kPackedBytes = int64_t(128) << 20;
 
-bool cut(int64_t tokens, int64_t dim, int64_t vocab, Cut* c) {
-    if (tokens < 0 || tokens > kMaxTokens || dim < 0 || dim > kMaxDim || vocab < 0 || vocab > kMaxVocab)
-        return false;
-    if (tokens > 0 && (dim < 1 || vocab < 1)) return false;
+void cut_piece(int64_t tokens, int64_t dim, int64_t vocab, bool packed, Cut* c) {
     c->dim_pad = up(dim > 0 ? dim : 1, 64);
     const int64_t t = tokens > 0 ? tokens : 1, v = up(vocab > 0 ? vocab : 1, 256);
-    int64_t piece = kPBytes / (2 * t);
-    if (kWBytes / (2 * c->dim_pad) < piece) piece = kWBytes / (2 * c->dim_pad);
+    int64_t piece = (packed ? kPackedBytes : kPBytes) / (2 * t);
+    if (packed && kPackedBytes / (2 * c->dim_pad) < piece) piece = kPackedBytes / (2 * c->dim_pad);
     piece = piece / 256 * 256;
     c->piece = piece < 256 ? 256 : (piece > v ? v : piece);
     c->slots = t <= kFewTokens ? v / 16 : v / 64;
@@ -766,14 +830,23 @@ bool cut(int64_t tokens, int64_t dim, int64_t vocab, Cut* c) {
     c->dx_slices = slices(dim_tiles * (up(t, 128) / 128), c->piece);
     c->dw_slices = slices(dim_tiles * (up(c->piece, 128) / 128), t);
     c->x_bytes = round_up(static_cast<size_t>(t * c->dim_pad) * 2, 256);
-    c->w_bytes = round_up(static_cast<size_t>(c->piece * c->dim_pad) * 2, 256);
+    c->row_bytes = 256 + round_up(static_cast<size_t>(t) * 16, 256);
+    c->w_bytes = packed ? round_up(static_cast<size_t>(c->piece * c->dim_pad) * 2, 256) : 0;
     c->p_bytes = round_up(static_cast<size_t>(t * c->piece) * 2, 256);
     size_t slab = static_cast<size_t>(c->dx_slices) * t * c->dim_pad * 4;
     if (c->dw_slices > 1) slab += static_cast<size_t>(c->dw_slices) * c->piece * c->dim_pad * 4;
     c->slab_bytes = round_up(slab, 256);
     c->part_bytes = round_up(static_cast<size_t>(c->slots) * t * 8, 256) + round_up(static_cast<size_t>(t) * 4, 256);
-    const size_t back = c->p_bytes + c->slab_bytes;
+    const size_t back = c->row_bytes + c->p_bytes + c->slab_bytes;
     c->total = c->x_bytes + c->w_bytes + (back > c->part_bytes ? back : c->part_bytes);
+}
+
+// False for sizes out of range.
+bool cut(int64_t tokens, int64_t dim, int64_t vocab, bool packed, Cut* c) {
+    if (tokens < 0 || tokens > kMaxTokens || dim < 0 || dim > kMaxDim || vocab < 0 || vocab > kMaxVocab)
+        return false;
+    if (tokens > 0 && (dim < 1 || vocab < 1)) return false;
+    cut_piece(tokens, dim, vocab, packed, c);
     return true;
 }
 
@@ -786,11 +859,10 @@ unsigned blocks_for(int64_t n) {
 template <int DT, Layout LA, Layout LB, Epilogue E, int BM, int BN, int WM, int WN>
 void launch_tiles(Product q, int slices, hipStream_t st) {
     q.tiles_m = (q.m + BM - 1) / BM;
-    q.tiles_n = (q.n + BN - 1) / BN;
     q.slices = slices;
     // as many blocks as the CUs' LDS holds at once
     constexpr int kBlocks = kCus * (kLdsBytes / (5 * (BM > BN ? BM : BN) * kTileK * 2));
-    const int total = q.tiles_m * q.tiles_n * slices;
+    const int total = q.tiles_m * ((q.n + BN - 1) / BN) * slices;
     hipLaunchKernelGGL((product_kernel<DT, LA, LB, E, BM, BN, WM, WN>),
                        dim3(static_cast<unsigned>(total < kBlocks ? total : kBlocks)), dim3(WM * WN * 64), 0, st, q);
 }
@@ -882,16 +954,25 @@ int forward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
 template <int DT>
 int backward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
     char* ws = static_cast<char*>(a->workspace);
-    char* xr = ws;
-    char* wr = ws + c.x_bytes;
+    unsigned short* xg = reinterpret_cast<unsigned short*>(ws);
+    int32_t* kept = reinterpret_cast<int32_t*>(ws + c.x_bytes);
+    int64_t* target = reinterpret_cast<int64_t*>(ws + c.x_bytes + 256);
+    float* lse = reinterpret_cast<float*>(target + a->tokens);
+    int32_t* rank = reinterpret_cast<int32_t*>(lse + a->tokens);
+    char* wr = ws + c.x_bytes + c.row_bytes;
     char* p16 = wr + c.w_bytes;
     float* dx_slab = reinterpret_cast<float*>(p16 + c.p_bytes);
     float* dw_slab = dx_slab + static_cast<int64_t>(c.dx_slices) * a->tokens * c.dim_pad;
+    const int tokens = static_cast<int>(a->tokens);
+    const int chunk = tokens / 1024 > 16 ? tokens / 1024 : 16;
+    hipLaunchKernelGGL(gather_kernel, dim3(static_cast<unsigned>((tokens + chunk - 1) / chunk)), dim3(256), 0, st,
+                       static_cast<const unsigned short*>(a->x), a->x_stride, a->dim, c.dim_pad, a->target, a->lse,
+                       a->vocab, tokens, chunk, xg, target, lse, rank, kept);
+    const Matrix x = {reinterpret_cast<const char*>(xg), c.dim_pad * 2, static_cast<int32_t>(c.dim_pad)};
     // fp16 holds 2^-24 at best, a probability of a large vocabulary is often
     // less: P is held times 2^15 there (at most 32768, below fp16's 65504)
     const float pscale = DT == ZERO_FP16 ? 32768.0f : 1.0f;
     const float grad = static_cast<float>(a->grad_scale / pscale);
-    const Matrix x = prepared(a->x, a->x_stride, 0, a->tokens, a->dim, c.dim_pad, xr, st);
     for (int64_t v = 0; v < a->vocab; v += c.piece) {
         const int64_t rows = a->vocab - v < c.piece ? a->vocab - v : c.piece;
         const Matrix w = prepared(a->w, a->w_stride, v, rows, a->dim, c.dim_pad, wr, st);
@@ -906,8 +987,9 @@ int backward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
         q.k = kdim;
         q.slice = static_cast<int32_t>(up(q.k, kTileK));
         q.first_m = static_cast<int32_t>(v);
-        q.target = a->target;
-        q.lse = a->lse;
+        q.target = target;
+        q.lse = lse;
+        q.kept = kept;
         q.vocab = static_cast<int32_t>(a->vocab);
         q.c = p16;
         q.ldc = c.piece;
@@ -928,6 +1010,7 @@ int backward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
         d.ldc = c.dim_pad;
         d.slab = a->tokens * c.dim_pad;
         d.add = v > 0;
+        d.kept = kept;
         launch_product<DT, kCols, kRows, kSlab>(d, c.dx_slices, st);
 
         // dw = P^T x: k is the tokens
@@ -939,6 +1022,7 @@ int backward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
         e.m = x.dim;
         e.n = q.m;
         e.k = q.n;
+        e.kept = kept;
         unsigned short* dw = static_cast<unsigned short*>(a->dw) + v * a->dw_stride;
         if (c.dw_slices > 1) {
             e.slice = static_cast<int32_t>(up(up(e.k, c.dw_slices) / c.dw_slices, kTileK));
@@ -948,8 +1032,8 @@ int backward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
             launch_product<DT, kCols, kCols, kSlab>(e, c.dw_slices, st);
             hipLaunchKernelGGL((slab_sum_kernel<DT>),
                                dim3(blocks_for(rows * (c.dim_pad / 4))), dim3(256), 0, st,
-                               dw_slab, c.dw_slices, e.slab, rows, a->dim, c.dim_pad, a->result, grad, dw,
-                               a->dw_stride);
+                               dw_slab, c.dw_slices, e.slab, rows, a->dim, c.dim_pad, a->result, grad, nullptr,
+                               dw, a->dw_stride);
         } else {
             e.slice = static_cast<int32_t>(up(e.k, kTileK));
             e.c = reinterpret_cast<char*>(dw);
@@ -963,7 +1047,7 @@ int backward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
     hipLaunchKernelGGL((slab_sum_kernel<DT>),
                        dim3(blocks_for(a->tokens * (c.dim_pad / 4))), dim3(256), 0, st,
                        dx_slab, c.dx_slices, a->tokens * c.dim_pad, a->tokens, a->dim, c.dim_pad, a->result, grad,
-                       static_cast<unsigned short*>(a->dx), a->dx_stride);
+                       rank, static_cast<unsigned short*>(a->dx), a->dx_stride);
     return launch_error("loss gradient kernel launch");
 }
 
@@ -975,8 +1059,10 @@ using namespace zero;
 extern "C" {
 
 size_t zero_xent_workspace_bytes(int64_t tokens, int64_t dim, int64_t vocab) {
-    Cut c;
-    return cut(tokens, dim, vocab, &c) ? c.total : 0;
+    // room for either layout of w
+    Cut whole, packed;
+    if (!cut(tokens, dim, vocab, false, &whole) || !cut(tokens, dim, vocab, true, &packed)) return 0;
+    return dim % 8 == 0 && whole.total > packed.total ? whole.total : packed.total;
 }
 
 int zero_xent_forward(const zero_xent_args* a, void* stream) {
@@ -986,7 +1072,7 @@ int zero_xent_forward(const zero_xent_args* a, void* stream) {
     hipStream_t st = static_cast<hipStream_t>(stream);
     if (a->tokens > 0) {
         Cut c;
-        cut(a->tokens, a->dim, a->vocab, &c);
+        cut(a->tokens, a->dim, a->vocab, !whole_pieces(a->w, a->w_stride, a->dim), &c);
         rc = a->dtype == ZERO_BF16 ? forward<ZERO_BF16>(a, c, st) : forward<ZERO_FP16>(a, c, st);
         if (rc) return rc;
     }
@@ -1007,7 +1093,7 @@ int zero_xent_backward(const zero_xent_args* a, void* stream) {
         return launch_error("loss gradient kernel launch");
     }
     Cut c;
-    cut(a->tokens, a->dim, a->vocab, &c);
+    cut(a->tokens, a->dim, a->vocab, !whole_pieces(a->w, a->w_stride, a->dim), &c);
     return a->dtype == ZERO_BF16 ? backward<ZERO_BF16>(a, c, st) : backward<ZERO_FP16>(a, c, st);
 }
 
