@@ -251,3 +251,14 @@ def test_masked_rows_reach_no_sum(size, bad):
     loss = c.args.loss.cpu().double()
     assert bool(((loss - r["loss"]).abs() <= b["loss"]).all()) and c.result().count == int((~masked).sum())
     assert not bool(c.d_dx[masked.cuda()].any())
+
+
+# where the forward changes its kernel, and k that ends inside a wave's share
+@pytest.mark.parametrize("size", [(8, 72, 130), (9, 72, 130), (7, 1096, 100), (1, 2056, 50000), (8, 520, 33),
+                                  (33, 4104, 300)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+def test_few_tokens(size, dtype):
+    say("%s %s" % (size, dtype))
+    c = Call(*size, dtype)
+    c.run()
+    c.check()

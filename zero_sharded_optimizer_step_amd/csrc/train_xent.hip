@@ -109,8 +109,8 @@ __device__ __forceinline__ f32x4 taken(const f32x4& c) { return f32x4{taken(c, 0
 template <Layout L, int R, int THREADS>
 struct Operand {
     static constexpr int kPieces = R * kTileK / 8;          // of 16 bytes
-    static_assert(kPieces % 64 == 0, "whole waves load");
-    static constexpr int kLoads = (kPieces + THREADS - 1) / THREADS;
+    static_assert(kPieces % THREADS == 0, "every thread loads");
+    static constexpr int kLoads = kPieces / THREADS;
     static constexpr int kRowPieces = L == kRows ? kTileK / 8 : R / 8;
     static constexpr int kRowsALoad = THREADS / kRowPieces;
     // a thread's later loads are the same piece of later rows, or in turn two pieces
@@ -163,9 +163,6 @@ struct Operand {
     }
     __device__ __forceinline__ void load(const Step& s, ZERO_LDS char* lds, int j) const {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-        if constexpr (kPieces < THREADS) {
-            if (wave * 64 >= kPieces) return;
-        }
         const __amdgpu_buffer_rsrc_t r =
             __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(s.at), 0, s.bytes, 0x00020000);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (ZERO_LDS void*)(lds + (j * THREADS + wave * 64) * 16), 16,
@@ -262,6 +259,7 @@ template <int DT, Layout LA, Layout LB, Epilogue E, int BM, int BN, int WM, int 
 __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) {
     constexpr int kThreads = WM * WN * 64;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;     // fragments of a wave
+    static_assert(FM % 2 == 0 && FN >= 4, "the epilogues' pairs and shares");
     typedef Operand<LA, BM, kThreads> OpA;
     typedef Operand<LB, BN, kThreads> OpB;
     constexpr int kSlot = (BM > BN ? BM : BN) * kTileK * 2;
@@ -351,7 +349,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                     char* to) __attribute__((always_inline)) -> void {
         constexpr int kItems = FM + FN + std::decay_t<decltype(op)>::kLoads;
         constexpr int kLoads = std::decay_t<decltype(op)>::kLoads;
-        constexpr int kSpan = FM * FN / 2 > 0 ? FM * FN / 2 : 1;
+        constexpr int kSpan = FM * FN / 2;
         // hidden, or every address of every slot takes a register of its own
         uint32_t fa = at_a, fb = at_b;
         asm volatile("" : "+v"(fa), "+v"(fb));
@@ -392,12 +390,12 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
         // the next tile's first loads, a share with each of the first four columns
         auto columns = [&](auto column) __attribute__((always_inline)) -> void {
             each<FN>([&](auto index) __attribute__((always_inline)) -> void {
-                constexpr int j = decltype(index)::value, kShares = FN < 4 ? FN : 4;
+                constexpr int j = decltype(index)::value;
                 __builtin_amdgcn_sched_barrier(0);
                 if (more) {
                     each<4>([&](auto share) __attribute__((always_inline)) -> void {
                         constexpr int g = decltype(share)::value;
-                        if constexpr (g * kShares / 4 == j) first_loads(g);
+                        if constexpr (g == j) first_loads(g);
                     });
                 }
                 column(index);
@@ -586,6 +584,90 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
     }
 }
 
+// kLse of up to 8 tokens: w is read once and nothing else counts, so the
+// fragments go from memory to registers, many loads at a time.  A block takes
+// 16 rows of w; its four waves take every fourth 64 of k, and the sums meet
+// in LDS in a fixed order.  Whole forward at dim 4096 in bf16 and that of the
+// 128 x 128 tiles: 1 token x 32000 54 us (4.9 TB/s) and 64, 1 x 128000 180 us
+// (5.8 TB/s) and 203, 8 x 32000 65 and 72, but 16 x 32000 89 and 78, since
+// every block reads x again.
+template <int DT>
+__global__ __launch_bounds__(256) void few_kernel(const Product q) {
+    constexpr int kGroup = 2;                              // of 64 k a wave and turn
+    __shared__ f32x4 s_sum[4][64];
+    const int lane = threadIdx.x & 63, s = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int m0 = blockIdx.x * 16;
+    auto records = [](int64_t bytes) { return static_cast<int>(bytes < 0x7ffffff0 ? bytes : 0x7ffffff0); };
+    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(q.a + m0 * q.lda), 0, records((q.m - m0) * q.lda), 0x00020000);
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(q.b), 0,
+                                                                        records(q.n * q.ldb), 0x00020000);
+    const uint32_t oa = static_cast<uint32_t>(s * q.lda), ob = static_cast<uint32_t>(s * q.ldb);
+    struct Pieces {
+        u32x4 a[kGroup][2], b[kGroup][2];
+    };
+    // k of this lane's piece p of block `block` of 64: both operands agree on it
+    auto load = [&](Pieces& f, int block) __attribute__((always_inline)) -> void {
+        #pragma unroll
+        for (int u = 0; u < kGroup; ++u)
+            #pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int k = (block + 4 * u) * 64 + g * 16 + p * 8;
+                f.a[u][p] = __builtin_amdgcn_raw_buffer_load_b128(ra, k < q.k ? oa + k * 2 : kNowhere, 0, 0);
+                f.b[u][p] = __builtin_amdgcn_raw_buffer_load_b128(rb, k < q.k ? ob + k * 2 : kNowhere, 0, 0);
+            }
+    };
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto multiply = [&](const Pieces& f) __attribute__((always_inline)) -> void {
+        #pragma unroll
+        for (int u = 0; u < kGroup; ++u)
+            #pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                if constexpr (DT == ZERO_BF16)
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, f.a[u][p]),
+                                                                  __builtin_bit_cast(bf16x8, f.b[u][p]), acc, 0, 0, 0);
+                else
+                    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, f.a[u][p]),
+                                                                 __builtin_bit_cast(f16x8, f.b[u][p]), acc, 0, 0, 0);
+            }
+    };
+    const int blocks = (q.k + 63) / 64;
+    Pieces f0, f1;
+    load(f0, wave);
+    for (int b = wave; b < blocks; b += 8 * kGroup) {
+        load(f1, b + 4 * kGroup);
+        multiply(f0);
+        load(f0, b + 8 * kGroup);
+        multiply(f1);
+    }
+    s_sum[wave][lane] = acc;
+    __syncthreads();
+    if (wave != 0) return;
+    const f32x4 c1 = s_sum[1][lane], c2 = s_sum[2][lane], c3 = s_sum[3][lane];
+    float x[4], top = -__builtin_inff(), sum = 0.0f;
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        x[e] = (acc[e] + c1[e]) + (c2[e] + c3[e]);
+        if (m0 + g * 4 + e >= q.m) x[e] = -__builtin_inff();
+        top = fmaxf(top, x[e]);
+    }
+    top = fmaxf(other_row(top).x, other_row(top).y);
+    top = fmaxf(other_half(top).x, other_half(top).y);
+    const float base = infinite(top) ? 0.0f : top;
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) sum += __expf(x[e] - base);
+    sum = other_row(sum).x + other_row(sum).y;
+    sum = other_half(sum).x + other_half(sum).y;
+    if (s >= q.n) return;
+    if (g == 0)
+        reinterpret_cast<f32x2*>(q.partial)[static_cast<int64_t>(q.slot0 + blockIdx.x) * q.n + s] = f32x2{top, sum};
+    const int64_t at = q.target[s] - q.first_m - m0 - g * 4;
+    #pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (at == e && m0 + g * 4 + e < q.m) q.target_logit[s] = x[e];
+}
+
 // ------------------------------------------------------- joining the partials
 __device__ __forceinline__ void write_mean(double sum, int64_t count, int beyond, zero_xent_result_t* out) {
     const double n = count > 1 ? static_cast<double>(count) : 1.0;
@@ -637,8 +719,8 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(const f32x2* __restrict
 }
 
 // Up to 16 tokens: one block joins the slots of all of them and the mean, so
-// that scoring a token takes two launches (with the two kernels above and
-// below, 4096 x 32000 in bf16 takes 67 us instead of @FEW@).
+// that scoring a token takes two launches: one token x 4096 x 32000 in bf16,
+// with w in the last-level cache, takes 41 us, with three launches 67.
 __global__ __launch_bounds__(1024) void xent_few_kernel(const f32x2* __restrict__ partial, int slots, int tokens,
                                                         const float* __restrict__ target_logit,
                                                         const int64_t* __restrict__ target, int64_t vocab,
@@ -866,7 +948,7 @@ struct Cut {
 };
 
 constexpr int64_t kMaxTokens = int64_t(1) << 20, kMaxDim = int64_t(1) << 20, kMaxVocab = int64_t(1) << 24;
-constexpr int64_t kFewTokens = 16;            // one tile of tokens in the forward
+constexpr int64_t kFewTokens = 8;             // few_kernel's rule
 // Beside a row of P, so that the rows of one column lie in unlike channels of
 // memory (gradient of 4096 x 4096 x 128000: 9.53 ms without, 9.45 with).
 constexpr int64_t kPPad = 192;
@@ -998,12 +1080,12 @@ int forward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
         q.partial = partial;
         q.target_logit = hit;
         q.vocab = static_cast<int32_t>(a->vocab);
-        if (tiles_of(q, 256, 256) >= 192) {
+        if (a->tokens <= kFewTokens) {
+            hipLaunchKernelGGL((few_kernel<DT>), dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0, st, q);
+            slots += static_cast<int>((rows + 15) / 16);
+        } else if (tiles_of(q, 256, 256) >= 192) {
             launch_tiles<DT, kRows, kRows, kLse, 256, 256, 2, 2>(q, 1, st);
             slots += static_cast<int>(up(rows, 256) / 256 * 2);
-        } else if (a->tokens <= kFewTokens) {
-            launch_tiles<DT, kRows, kRows, kLse, 64, 16, 4, 1>(q, 1, st);
-            slots += static_cast<int>(up(rows, 64) / 64 * 4);
         } else {
             launch_tiles<DT, kRows, kRows, kLse, 128, 128, 2, 2>(q, 1, st);
             slots += static_cast<int>(up(rows, 128) / 128 * 2);
