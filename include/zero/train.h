@@ -184,7 +184,10 @@ int zero_tensors_scalars(const zero_tensors_args* a, zero_tensors_scalars_t* out
  *   P_ij = grad_scale / max(1, count) * (exp(logits_ij - lse_i) - [j = target_i])
  *   dx = P w,  dw = P^T x.
  * The logits are formed piece by piece of the vocabulary and never kept:
- * the backward forms them again.  Products are of the 16-bit inputs with
+ * the backward forms them again, of the tokens that have a target only.  A
+ * token without one has an lse like any other, but its row of x reaches no
+ * other token's loss and neither the mean nor dw, whatever it holds (NaN and
+ * infinities too), and its row of dx is zero.  Products are of the 16-bit inputs with
  * fp32 sums; loss and lse are fp32; the sum over tokens is fp64 in a fixed
  * order.  P is rounded to 16 bits for the two products of the gradient
  * (a relative half step of the dtype, what dx and dw are rounded by too).

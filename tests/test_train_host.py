@@ -219,3 +219,17 @@ def test_binding_refuses_buffers_shorter_than_the_call_touches():
         Z.zero_state8_encode(m, m, s8[:512], e8)
     with pytest.raises(ValueError):
         Z.zero_state8_decode(s8, e8, m, g)
+
+
+def test_binding_refuses_host_tensors():
+    x, w = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(9, 8, dtype=torch.bfloat16)
+    f, t = torch.zeros(4), torch.zeros(4, dtype=torch.int64)
+    args = Z.XentArgs(x=x, w=w, target=t, loss=f, lse=f, result=torch.zeros(32, dtype=torch.uint8),
+                      workspace=torch.zeros(1 << 16, dtype=torch.uint8), dx=x, dw=w)
+    m, g = torch.zeros(300), torch.zeros(300, dtype=torch.bfloat16)
+    s8, e8 = torch.zeros(1024, dtype=torch.uint8), torch.zeros(4, dtype=torch.uint8)
+    for call in (lambda: Z.zero_xent_forward(args), lambda: Z.zero_xent_backward(args),
+                 lambda: Z.TensorSet(master=[m], grad=[g], exp_avg=[m], exp_avg_sq=[m]),
+                 lambda: Z.zero_state8_encode(m, m, s8, e8), lambda: Z.zero_state8_decode(s8, e8, m, m)):
+        with pytest.raises(ValueError, match="device memory"):
+            call()

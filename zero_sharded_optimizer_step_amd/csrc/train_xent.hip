@@ -5,10 +5,12 @@
 //              per token and wave row, its largest logit and the sum of
 //              exponentials below it (one pass of a running softmax), and
 //              the target's logit; a second kernel joins them into lse and
-//              loss, a third sums the losses.
-//   backward   piece by piece of the vocabulary: L again, P = exp(L - lse) -
-//              onehot rounded to 16 bits into the workspace, then
-//              dx += P w (fp32 in the workspace) and dw = P^T x.
+//              loss, a third sums the losses.  Up to 8 tokens: w is read
+//              straight into registers, and one kernel joins it all.
+//   backward   the tokens that have a target are gathered; then piece by
+//              piece of the vocabulary: L again, P = exp(L - lse) - onehot
+//              rounded to 16 bits into the workspace, then dx += P w (fp32
+//              in the workspace) and dw = P^T x.
 //
 // One tile product serves all of it.  An operand lies with its rows along k
 // (x and w in the logits, P in dx) or with k as the row (w in dx; x and P in

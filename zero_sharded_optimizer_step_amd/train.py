@@ -20,6 +20,13 @@ from ._train_abi import (ZERO_MAX_GROUPS, ZERO_STATE8_BLOCK, train_lib, zero_ada
                          zero_tensors_scalars_t, zero_xent_args, zero_xent_result_t)
 
 
+def _on_device(**tensors) -> None:
+    """Refuse host tensors: their addresses would fault the GPU."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_cuda:
+            raise ValueError("%s is on %s; expected device memory" % (name, t.device))
+
+
 # ------------------------------------------------------------------ 8-bit states
 def state8_blocks(n: int) -> int:
     """Blocks of ZERO_STATE8_BLOCK elements that n elements take: 512 bytes
@@ -41,6 +48,7 @@ def zero_state8_encode(exp_avg, exp_avg_sq, state8, scale8, n: Optional[int] = N
     _need(exp_avg, 4 * n, "exp_avg")
     _need(exp_avg_sq, 4 * n, "exp_avg_sq")
     _need_state8(state8, scale8, n)
+    _on_device(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, state8=state8, scale8=scale8)
     check(train_lib().zero_state8_encode(_dptr(exp_avg), _dptr(exp_avg_sq), n, _dptr(state8),
                                          _dptr(scale8), _stream(stream)), "zero_state8_encode")
 
@@ -55,6 +63,7 @@ def zero_state8_decode(state8, scale8, exp_avg, exp_avg_sq, n: Optional[int] = N
     _need(exp_avg, exp_avg.element_size() * n, "exp_avg")
     _need(exp_avg_sq, exp_avg_sq.element_size() * n, "exp_avg_sq")
     _need_state8(state8, scale8, n)
+    _on_device(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, state8=state8, scale8=scale8)
     check(train_lib().zero_state8_decode(_dptr(state8), _dptr(scale8), n, _dptr(exp_avg),
                                          _dptr(exp_avg_sq), dtype_code(exp_avg.dtype), _stream(stream)),
           "zero_state8_decode")
@@ -137,6 +146,8 @@ class TensorSet:
                 _need_state8(first[t], second[t], numel)
             if param is not None:
                 _need(param[t], 2 * numel, "param[%d]" % t)
+            _on_device(master=master[t], grad=grad[t], exp_avg=first[t], exp_avg_sq=second[t],
+                       param=param[t] if param is not None else None)
             recs.append(zero_tensor_t(_dptr(grad[t]), _dptr(master[t]), _dptr(first[t]), _dptr(second[t]),
                                       _dptr(param[t]) if param is not None else None, numel, group[t], 0))
         self._keep = (master, grad, first, second, param)
@@ -269,6 +280,8 @@ class XentArgs:
             _need(m, 4 * t, name)
         _need(self.target, 8 * t, "target")
         _need(self.result, ctypes.sizeof(zero_xent_result_t), "result")
+        _on_device(x=x, w=w, target=self.target, loss=self.loss, lse=self.lse, result=self.result,
+                   workspace=self.workspace, dx=self.dx if backward else None, dw=self.dw if backward else None)
         a.target, a.loss, a.lse = _dptr(self.target), _dptr(self.loss), _dptr(self.lse)
         a.result = _dptr(self.result)
         a.grad_scale = self.grad_scale
