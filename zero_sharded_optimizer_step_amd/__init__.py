@@ -76,6 +76,11 @@ def tiled_state_numel(shard_numel: int) -> int:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
+        c = _torch()._C
+        # the same handle without building a Stream object, which costs more
+        # than the rest of a small call's binding
+        if hasattr(c, "_cuda_getCurrentRawStream"):
+            return c._cuda_getCurrentRawStream(_torch().cuda.current_device())
         return _torch().cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream

@@ -158,6 +158,7 @@ class TensorSet:
         self.table = torch.frombuffer(table, dtype=torch.uint8).to(device)
         self.workspace = torch.empty(self.plan.workspace_bytes, dtype=torch.uint8, device=device)
         self.result = torch.zeros(32, dtype=torch.uint8, device=device)
+        self._group_values = None
         a = self._c = zero_tensors_args()
         a.plan = self.plan
         a.table = _dptr(self.table)
@@ -171,10 +172,12 @@ class TensorSet:
         """The zero_tensors_args of a call; `scalars` is a device copy of a
         zero_tensors_scalars_t (288 bytes) or None."""
         a = self._c
-        self._groups = (zero_adam_group_t * max(len(groups), 1))(
-            *[(g.lr, g.beta1, g.beta2, g.eps, g.weight_decay) for g in groups])
-        a.groups = self._groups
-        a.n_groups = len(groups)
+        values = [(g.lr, g.beta1, g.beta2, g.eps, g.weight_decay) for g in groups]
+        if values != self._group_values:
+            self._groups = (zero_adam_group_t * max(len(values), 1))(*values)
+            a.groups = self._groups
+            a.n_groups = len(values)
+            self._group_values = values
         a.step = step
         a.loss_scale = loss_scale
         a.grad_predivide = grad_predivide
@@ -182,7 +185,9 @@ class TensorSet:
         a.peer_sumsq = peer_sumsq
         a.peer_overflow = 1 if peer_overflow else 0
         a.seed = seed & 0xFFFFFFFFFFFFFFFF
-        _need(scalars, ctypes.sizeof(zero_tensors_scalars_t), "scalars")
+        if scalars is not None:
+            _need(scalars, ctypes.sizeof(zero_tensors_scalars_t), "scalars")
+            _on_device(scalars=scalars)
         a.scalars = _dptr(scalars)
         return a
 
