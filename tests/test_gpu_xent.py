@@ -262,3 +262,72 @@ def test_few_tokens(size, dtype):
     c = Call(*size, dtype)
     c.run()
     c.check()
+
+
+def on_gpu(c):
+    """A call's outputs against the definition computed in fp64 on the GPU."""
+    x, w = c.d_x.contiguous(), c.d_w.contiguous()
+    r = train_ref.xent(x, w, c.args.target, c.args.grad_scale)
+    b = train_ref.xent_bounds(r, x, w, c.dtype)
+    for name in ("loss", "lse", "dx", "dw"):
+        got = getattr(c, "d_" + name) if name in ("dx", "dw") else getattr(c.args, name)
+        err = (got.double() - r[name]).abs()
+        say("  %-4s worst error %.3g of its bound" % (name, (err / b[name].clamp(min=1e-300)).max().item()))
+        assert bool((err <= b[name]).all()), name
+
+
+# every product in 256 x 256 tiles that end oddly, from the caller's rows and from repacked ones
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("size", [(4100, 3080, 4104), (4100, 3079, 4099)], ids=lambda s: "x".join(map(str, s)))
+def test_large_tiles(size, dtype):
+    say("%s %s" % (size, dtype))
+    c = Call(*size, dtype, ignored=0.05)
+    c.run()
+    on_gpu(c)
+
+
+# w past 2^31 elements and 2^32 bytes
+@pytest.mark.parametrize("tokens", [2, 40])
+def test_offsets_past_32_bits(tokens):
+    vocab, dim = 300000, 8192
+    say("%d tokens" % tokens)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.empty(vocab, dim, dtype=torch.bfloat16, device="cuda").normal_(0.0, 3.0 / dim**0.5, generator=g)
+    x = torch.randn(tokens, dim, generator=g, device="cuda").to(torch.bfloat16)
+    target = torch.randint(vocab - 1000, vocab, (tokens,), generator=g, device="cuda")
+    a = Z.XentArgs(x=x, w=w, target=target, loss=torch.empty(tokens, device="cuda"),
+                   lse=torch.empty(tokens, device="cuda"), result=torch.zeros(32, dtype=torch.uint8, device="cuda"),
+                   workspace=torch.empty(Z.zero_xent_workspace_bytes(tokens, dim, vocab), dtype=torch.uint8,
+                                         device="cuda"), dx=torch.empty_like(x), dw=torch.full_like(w, 9.0))
+    Z.zero_xent_forward(a)
+    Z.zero_xent_backward(a)
+    logits = torch.empty(tokens, vocab, dtype=torch.float64, device="cuda")
+    size = torch.empty_like(logits)
+    for v in range(0, vocab, 50000):
+        logits[:, v:v + 50000] = x.double() @ w[v:v + 50000].double().t()
+        size[:, v:v + 50000] = x.double().abs() @ w[v:v + 50000].double().abs().t()
+    lse = torch.logsumexp(logits, 1)
+    rows = torch.arange(tokens, device="cuda")
+    loss = lse - logits[rows, target]
+    soft = (logits - lse[:, None]).exp()
+    p = soft.clone()
+    p[rows, target] -= 1.0
+    r = {"loss": loss, "lse": lse, "p": p, "soft": soft, "kept": torch.ones(tokens, dtype=torch.bool, device="cuda"),
+         "at": target, "c": 1.0 / tokens, "size": size}
+    # the bounds of slices of w's rows: those of dx add up
+    bound_dx, dx = torch.zeros(tokens, dim, dtype=torch.float64, device="cuda"), torch.zeros_like(x, dtype=torch.float64)
+    u = torch.finfo(torch.bfloat16).eps / 2
+    e_row = (dim * 2.0**-23 * size).amax(1)
+    dp = p.abs() * u + soft * (2 * e_row + 2.0**-19)[:, None] + 2.0**-134
+    dp[rows, target] += 2.0**-23
+    assert bool(((a.lse.double() - lse).abs() <= e_row + 2.0**-20 + 2.0**-22 * lse.abs()).all())
+    assert bool(((a.loss.double() - loss).abs() <= 2 * e_row + 2.0**-20 + 2.0**-22 * (lse.abs() + (lse - loss).abs())).all())
+    for v in range(0, vocab, 50000):
+        part, wv = slice(v, v + 50000), w[v:v + 50000].double()
+        dx += r["c"] * (p[:, part] @ wv)
+        bound_dx += r["c"] * (dp[:, part] @ wv.abs() + vocab * 2.0**-23 * (p[:, part].abs() @ wv.abs())) * (1 + u)
+        dw = r["c"] * (p[:, part].t() @ x.double())
+        bound = r["c"] * (dp[:, part].t() @ x.double().abs() +
+                          tokens * 2.0**-23 * (p[:, part].abs().t() @ x.double().abs())) * (1 + u) + u * dw.abs() + 2.0**-134
+        assert bool(((a.dw[part].double() - dw).abs() <= bound).all()), v
+    assert bool(((a.dx.double() - dx).abs() <= bound_dx + u * dx.abs() + 2.0**-134).all())
