@@ -331,3 +331,36 @@ def test_offsets_past_32_bits(tokens):
                           tokens * 2.0**-23 * (p[:, part].abs().t() @ x.double().abs())) * (1 + u) + u * dw.abs() + 2.0**-134
         assert bool(((a.dw[part].double() - dw).abs() <= bound).all()), v
     assert bool(((a.dx.double() - dx).abs() <= bound_dx + u * dx.abs() + 2.0**-134).all())
+
+
+# the same in tiles of 128 x 128 and of 256 x 256: columns of -inf, rows of NaN, all -inf
+@pytest.mark.parametrize("size", [(20, 64, 300), (300, 64, 40000)], ids=lambda s: "x".join(map(str, s)))
+def test_infinite_logits_in_tiles(size):
+    c = Call(*size, torch.bfloat16, ignored=0.0)
+    c.d_x.abs_().clamp_(min=0.25)                # x > 0: the columns below are -inf
+    c.d_w[7:150] = -float("inf")
+    c.d_x[2] = float("nan")
+    c.d_w[200, 0] = 2.0
+    c.d_x[4, 0] = float("inf")                   # its logits are +-inf and NaN
+    c.args.target[:] = 220
+    c.run(backward=False)
+    x, w = c.d_x.double().contiguous(), c.d_w.double().contiguous()
+    rest = torch.ones(size[0], dtype=torch.bool, device="cuda")
+    rest[2] = rest[4] = False
+    alive = torch.ones(size[2], dtype=torch.bool, device="cuda")
+    alive[7:150] = False
+    logits = x[rest] @ w[alive].t()
+    want = torch.logsumexp(logits, 1)
+    # as train_ref.xent_bounds has it
+    bound = (64 * 2.0**-23 * (x[rest].abs() @ w[alive].abs().t())).amax(1) + 2.0**-20 + 2.0**-22 * want.abs()
+    got = c.args.lse.double()
+    assert bool(((got[rest] - want).abs() <= bound).all())
+    assert bool(torch.isnan(got[2])) and not bool(torch.isfinite(got[4]))
+    # a target on a -inf column: an infinite loss, no NaN
+    c.args.target[:] = 10
+    c.run(backward=False)
+    assert bool((c.args.loss[rest] == float("inf")).all())
+    c.d_w[:] = -float("inf")
+    c.d_x.fill_(1.0)
+    c.run(backward=False)
+    assert bool((c.args.lse == -float("inf")).all())
