@@ -278,7 +278,7 @@ def on_gpu(c):
 
 # every product in 256 x 256 tiles that end oddly, from the caller's rows and from repacked ones
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
-@pytest.mark.parametrize("size", [(4100, 3080, 4104), (4100, 3079, 4099)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("size", [(4100, 3080, 4104), (4100, 3079, 4099), (4000, 72, 3700), (4000, 65, 3701)], ids=lambda s: "x".join(map(str, s)))
 def test_large_tiles(size, dtype):
     say("%s %s" % (size, dtype))
     c = Call(*size, dtype, ignored=0.05)
@@ -334,7 +334,7 @@ def test_offsets_past_32_bits(tokens):
 
 
 # the same in tiles of 128 x 128 and of 256 x 256: columns of -inf, rows of NaN, all -inf
-@pytest.mark.parametrize("size", [(20, 64, 300), (300, 64, 40000)], ids=lambda s: "x".join(map(str, s)))
+@pytest.mark.parametrize("size", [(20, 64, 300), (300, 64, 40000), (3900, 64, 3900)], ids=lambda s: "x".join(map(str, s)))
 def test_infinite_logits_in_tiles(size):
     c = Call(*size, torch.bfloat16, ignored=0.0)
     c.d_x.abs_().clamp_(min=0.25)                # x > 0: the columns below are -inf

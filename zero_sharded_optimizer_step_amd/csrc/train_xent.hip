@@ -243,9 +243,9 @@ __device__ __forceinline__ u32x4 pair(const f32x4 a, const f32x4 b, float f) {
 __device__ __forceinline__ bool infinite(float x) { return __builtin_fabsf(x) == __builtin_inff(); }
 
 // The product's tile by tile.  What bounds a large one is the matrix cores'
-// power: at 4096 tokens x 4096 x 128000 in bf16 the clock falls to 1.8 GHz,
-// and the forward takes 2.99 ms (1.44 PFLOP/s) with values of a normal
-// distribution and 2.56 ms with zeros.  Hence
+// power: at 4096 tokens x 4096 x 128000 in bf16 the clock falls to 1.85 GHz,
+// and the forward takes 2.95 to 3.0 ms (1.44 PFLOP/s) with values of a normal
+// distribution and 2.51 ms with zeros.  Hence
 //   - four waves with 128 x 128 of a 256 x 256 tile each, one a SIMD, so that
 //     a value out of LDS serves 8 products of 16 x 16 x 32 (eight waves of
 //     128 x 64 read half as much again: 3.35 ms with all of the below lacking);
@@ -1017,10 +1017,20 @@ void launch_tiles(Product q, int slices, hipStream_t st) {
 
 int64_t tiles_of(const Product& q, int64_t bm, int64_t bn) { return up(q.m, bm) / bm * (up(q.n, bn) / bn); }
 
-// Returns the wave rows of a tile and their extent in m (for kLse's slots).
+// 256 x 256 or 128 x 128: by how often each fills the chip, the larger one
+// block a CU, the smaller two, a round of the larger taking 1.6 times one of
+// the smaller.  Forward of 2048 tokens x 4096, 128 x 128 and 256 x 256: 4096
+// of the vocabulary (128 large tiles) 68 and 87 us, 5120 (160) 103 and 86,
+// 8192 (256) 124 and 103, 8448 (264) 153 and 174, 16384 (512) 238 and 196.
+bool large_tiles(const Product& q, int slices) {
+    const int64_t large = (tiles_of(q, 256, 256) * slices + kCus - 1) / kCus;
+    const int64_t small = (tiles_of(q, 128, 128) * slices + 2 * kCus - 1) / (2 * kCus);
+    return 8 * large <= 5 * small;
+}
+
 template <int DT, Layout LA, Layout LB, Epilogue E>
 void launch_product(const Product& q, int slices, hipStream_t st) {
-    if (tiles_of(q, 256, 256) * slices >= 192) launch_tiles<DT, LA, LB, E, 256, 256, 2, 2>(q, slices, st);
+    if (large_tiles(q, slices)) launch_tiles<DT, LA, LB, E, 256, 256, 2, 2>(q, slices, st);
     else launch_tiles<DT, LA, LB, E, 128, 128, 2, 2>(q, slices, st);
 }
 
@@ -1085,7 +1095,7 @@ int forward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
         if (a->tokens <= kFewTokens) {
             hipLaunchKernelGGL((few_kernel<DT>), dim3(static_cast<unsigned>((rows + 15) / 16)), dim3(256), 0, st, q);
             slots += static_cast<int>((rows + 15) / 16);
-        } else if (tiles_of(q, 256, 256) >= 192) {
+        } else if (large_tiles(q, 1)) {
             launch_tiles<DT, kRows, kRows, kLse, 256, 256, 2, 2>(q, 1, st);
             slots += static_cast<int>(up(rows, 256) / 256 * 2);
         } else {
