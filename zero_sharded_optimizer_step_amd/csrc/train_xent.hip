@@ -438,8 +438,24 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 for (int i = 1; i < FM; ++i) top = max3(x[i][0], x[i][1], max3(x[i][2], x[i][3], top));
                 top = fmaxf(other_row(top).x, other_row(top).y);
                 top = fmaxf(other_half(top).x, other_half(top).y);
-                // exp(x - top) as 2^(x log2 e - c) 2^(c - top log2 e)
-                const float base = infinite(top) ? 0.0f : top;
+                const bool hit = n < size_n && here<FM>(at[j]);
+                if (__builtin_amdgcn_ballot_w64(hit) != 0) {
+                    const float v = pick(x, at[j]);
+                    if (hit) q.target_logit[n] = v;
+                }
+                // exp(x - top) as 2^(x log2 e - c) 2^(c - top log2 e): the second
+                // factor is c's rounding, between 2^-1/16 and 2^1/16 up to kFar.
+                // Beyond it the factors would leave fp32's range (0 times inf),
+                // past 2.36e38 c itself: there top is subtracted first.
+                float base = infinite(top) ? 0.0f : top;
+                constexpr float kFar = 1 << 20;
+                if (__builtin_amdgcn_ballot_w64(__builtin_fabsf(base) > kFar) != 0) {
+                    #pragma unroll
+                    for (int i = 0; i < FM; ++i)
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e) x[i][e] -= base;
+                    base = 0.0f;
+                }
                 const float c = base * kLog2e, rest = __builtin_fmaf(base, -kLog2e, c);
                 f32x4 part = {0.0f, 0.0f, 0.0f, 0.0f}, y[FM];
                 #pragma unroll
@@ -457,11 +473,6 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 sum = other_half(sum).x + other_half(sum).y;
                 if (n < size_n && lane < 16)
                     reinterpret_cast<f32x2*>(q.partial)[static_cast<int64_t>(slot) * size_n + n] = f32x2{top, sum};
-                const bool hit = n < size_n && here<FM>(at[j]);
-                if (__builtin_amdgcn_ballot_w64(hit) != 0) {
-                    const float v = pick(x, at[j]);
-                    if (hit) q.target_logit[n] = v;
-                }
             };
             split(column);
         } else if constexpr (E == kProb) {
