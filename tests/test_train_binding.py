@@ -1,0 +1,48 @@
+"""CPU tests of the training operators' binding: what a TensorSet keeps, and
+the buffers that its calls refuse.  No call here reaches the HIP runtime."""
+import gc
+import weakref
+
+import numpy as np
+import pytest
+import torch
+
+import zero_sharded_optimizer_step_amd as Z
+from zero_sharded_optimizer_step_amd import train
+
+
+@pytest.fixture
+def anywhere(monkeypatch):
+    """Host tensors pass for device ones; nothing is launched."""
+    monkeypatch.setattr(train, "_on_device", lambda **tensors: None)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_set_keeps_the_memory_that_its_table_points_at(anywhere, bits):
+    # numpy arrays behind the tensors: they live as long as the memory is held
+    alive = {}
+
+    def fresh(name, n, dtype):
+        a = np.zeros(n, dtype)
+        alive[name] = weakref.ref(a)
+        return torch.from_numpy(a)
+    n, k = 300, Z.state8_blocks(300)
+    lists = {"master": [fresh("master", n, np.float32)], "grad": [fresh("grad", n, np.float16)],
+             "param": [fresh("param", n, np.float16)]}
+    if bits == 32:
+        lists.update(exp_avg=[fresh("m", n, np.float32)], exp_avg_sq=[fresh("v", n, np.float32)])
+    else:
+        # 16-byte aligned codes
+        lists.update(state8=[fresh("s", 512 * k + 16, np.uint8)], scale8=[fresh("e", 2 * k, np.uint8)])
+        lists["state8"][0] = lists["state8"][0][-lists["state8"][0].data_ptr() % 16:][:512 * k]
+    ts = Z.TensorSet(**lists)
+    # the caller puts other tensors in their places, in the lists and behind the tensors
+    lists["param"][0].data = torch.zeros(n, dtype=torch.float16)
+    for seq in lists.values():
+        seq[0] = None
+    lists["grad"].clear()
+    gc.collect()
+    assert all(r() is not None for r in alive.values()), [x for x, r in alive.items() if r() is None]
+    del ts
+    gc.collect()
+    assert all(r() is None for r in alive.values())

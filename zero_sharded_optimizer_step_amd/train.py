@@ -106,8 +106,11 @@ class TensorSet:
     state is `exp_avg` and `exp_avg_sq` (fp32) or `state8` and `scale8`
     (uint8, 512 and 2 bytes per block of 256 elements); `param` is the list of
     16-bit parameters to write, or None; `group[t]` is tensor t's group.
-    The set keeps the tensors alive and owns the table, the workspace and
-    `result`, the device zero_global_t of the last step (32 bytes)."""
+    The table holds their addresses: the set keeps that memory alive,
+    whatever becomes of the lists and tensors given here, and a tensor that
+    moves or is replaced (a gradient in new memory, say) needs a new set.
+    It owns the table, the workspace and `result`, the device zero_global_t
+    of the last step (32 bytes)."""
 
     def __init__(self, master, grad, exp_avg=None, exp_avg_sq=None, state8=None, scale8=None,
                  param=None, group: Optional[Sequence[int]] = None):
@@ -150,7 +153,9 @@ class TensorSet:
                        param=param[t] if param is not None else None)
             recs.append(zero_tensor_t(_dptr(grad[t]), _dptr(master[t]), _dptr(first[t]), _dptr(second[t]),
                                       _dptr(param[t]) if param is not None else None, numel, group[t], 0))
-        self._keep = (master, grad, first, second, param)
+        # tensors of the set's own on the same memory: the caller's lists may change
+        self._keep = [x.detach() for seq in (master, grad, first, second, param) if seq is not None
+                      for x in seq if x is not None]
         self.state_bits = bits
         self.plan, table = zero_tensors_plan(recs, bits, grad_dtype,
                                              0 if param_dtype is None else dtype_code(param_dtype))
