@@ -46,3 +46,21 @@ def test_a_set_keeps_the_memory_that_its_table_points_at(anywhere, bits):
     del ts
     gc.collect()
     assert all(r() is None for r in alive.values())
+
+
+def a_set():
+    m, g = torch.zeros(300), torch.zeros(300, dtype=torch.bfloat16)
+    return Z.TensorSet(master=[m], grad=[g], exp_avg=[m.clone()], exp_avg_sq=[m.clone()])
+
+
+def test_norm_and_apply_refuse_host_tensors(monkeypatch):
+    with monkeypatch.context() as m:
+        m.setattr(train, "_on_device", lambda **tensors: None)
+        ts = a_set()
+    groups = [Z.AdamGroup()]
+    table = torch.zeros(Z.zero_partials_bytes(2), dtype=torch.uint8)
+    # a stream's number, so that no call asks torch for the current one
+    with pytest.raises(ValueError, match="partials is on cpu"):
+        Z.zero_tensors_norm(ts, groups, 1, 0, table, stream=0)
+    with pytest.raises(ValueError, match="global_buf is on cpu"):
+        Z.zero_tensors_apply(ts, groups, 1, torch.zeros(32, dtype=torch.uint8), stream=0)

@@ -214,6 +214,7 @@ def zero_tensors_norm(tensors: TensorSet, groups: Sequence[AdamGroup], step: int
     """The set's partial sums into slot `slot` of a zero_partials_bytes
     table, for zero_shard_combine."""
     _need(partials, (slot + 1) * lib().zero_partials_bytes(1), "partials")
+    _on_device(partials=partials)
     check(train_lib().zero_tensors_norm(ctypes.byref(tensors.args(groups, step, **hyper)), slot,
                                         _dptr(partials), _stream(stream)), "zero_tensors_norm")
 
@@ -222,6 +223,7 @@ def zero_tensors_apply(tensors: TensorSet, groups: Sequence[AdamGroup], step: in
                        stream=None, **hyper) -> None:
     """The update by a zero_global_t in device memory."""
     _need(global_buf, ctypes.sizeof(zero_global_t), "global_buf")
+    _on_device(global_buf=global_buf)
     check(train_lib().zero_tensors_apply(ctypes.byref(tensors.args(groups, step, **hyper)),
                                          _dptr(global_buf), _stream(stream)), "zero_tensors_apply")
 
