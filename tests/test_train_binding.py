@@ -64,3 +64,38 @@ def test_norm_and_apply_refuse_host_tensors(monkeypatch):
         Z.zero_tensors_norm(ts, groups, 1, 0, table, stream=0)
     with pytest.raises(ValueError, match="global_buf is on cpu"):
         Z.zero_tensors_apply(ts, groups, 1, torch.zeros(32, dtype=torch.uint8), stream=0)
+
+
+def strided(n, dtype):
+    return torch.zeros(2 * n, dtype=dtype)[::2]
+
+
+def test_calls_refuse_buffers_that_are_not_contiguous(anywhere):
+    # the library gets an address only: a strided view would be read at the wrong
+    # elements, an expanded one past its memory
+    m, v = torch.zeros(300), torch.zeros(300)
+    s8, e8 = torch.zeros(1024, dtype=torch.uint8), torch.zeros(4, dtype=torch.uint8)
+    one, byte = torch.zeros(1), torch.zeros(1, dtype=torch.uint8)
+    good = {"exp_avg": m, "exp_avg_sq": v, "state8": s8, "scale8": e8}
+    for name, bad in (("exp_avg", strided(300, torch.float32)), ("exp_avg_sq", one.expand(300)),
+                      ("state8", byte.expand(1024)), ("scale8", strided(4, torch.uint8))):
+        kw = {**good, name: bad}
+        with pytest.raises(ValueError, match="%s is not contiguous" % name):
+            Z.zero_state8_encode(kw["exp_avg"], kw["exp_avg_sq"], kw["state8"], kw["scale8"], stream=0)
+        with pytest.raises(ValueError, match="%s is not contiguous" % name):
+            Z.zero_state8_decode(kw["state8"], kw["scale8"], kw["exp_avg"], kw["exp_avg_sq"], stream=0)
+    x, w = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(9, 8, dtype=torch.bfloat16)
+    f, t = torch.zeros(4), torch.zeros(4, dtype=torch.int64)
+    args = dict(x=x, w=w, target=t, loss=f, lse=f, result=torch.zeros(32, dtype=torch.uint8),
+                workspace=torch.zeros(1 << 16, dtype=torch.uint8), dx=x, dw=w)
+    for name, bad in (("result", byte.expand(32)), ("workspace", byte.expand(1 << 20))):
+        for backward in (False, True):
+            with pytest.raises(ValueError, match="%s is not contiguous" % name):
+                Z.XentArgs(**{**args, name: bad}).c_args(backward)
+    ts, groups = a_set(), [Z.AdamGroup()]
+    with pytest.raises(ValueError, match="partials is not contiguous"):
+        Z.zero_tensors_norm(ts, groups, 1, 0, byte.expand(Z.zero_partials_bytes(1)), stream=0)
+    with pytest.raises(ValueError, match="global_buf is not contiguous"):
+        Z.zero_tensors_apply(ts, groups, 1, strided(32, torch.uint8), stream=0)
+    with pytest.raises(ValueError, match="scalars is not contiguous"):
+        Z.zero_tensors_scalars(ts, groups, 1, scalars=byte.expand(288))

@@ -27,6 +27,14 @@ def _on_device(**tensors) -> None:
             raise ValueError("%s is on %s; expected device memory" % (name, t.device))
 
 
+def _contiguous(**tensors) -> None:
+    """Refuse strided and expanded tensors where the library goes by the
+    address alone."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError("%s is not contiguous" % name)
+
+
 # ------------------------------------------------------------------ 8-bit states
 def state8_blocks(n: int) -> int:
     """Blocks of ZERO_STATE8_BLOCK elements that n elements take: 512 bytes
@@ -48,6 +56,7 @@ def zero_state8_encode(exp_avg, exp_avg_sq, state8, scale8, n: Optional[int] = N
     _need(exp_avg, 4 * n, "exp_avg")
     _need(exp_avg_sq, 4 * n, "exp_avg_sq")
     _need_state8(state8, scale8, n)
+    _contiguous(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, state8=state8, scale8=scale8)
     _on_device(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, state8=state8, scale8=scale8)
     check(train_lib().zero_state8_encode(_dptr(exp_avg), _dptr(exp_avg_sq), n, _dptr(state8),
                                          _dptr(scale8), _stream(stream)), "zero_state8_encode")
@@ -63,6 +72,7 @@ def zero_state8_decode(state8, scale8, exp_avg, exp_avg_sq, n: Optional[int] = N
     _need(exp_avg, exp_avg.element_size() * n, "exp_avg")
     _need(exp_avg_sq, exp_avg_sq.element_size() * n, "exp_avg_sq")
     _need_state8(state8, scale8, n)
+    _contiguous(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, state8=state8, scale8=scale8)
     _on_device(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, state8=state8, scale8=scale8)
     check(train_lib().zero_state8_decode(_dptr(state8), _dptr(scale8), n, _dptr(exp_avg),
                                          _dptr(exp_avg_sq), dtype_code(exp_avg.dtype), _stream(stream)),
@@ -192,6 +202,7 @@ class TensorSet:
         a.seed = seed & 0xFFFFFFFFFFFFFFFF
         if scalars is not None:
             _need(scalars, ctypes.sizeof(zero_tensors_scalars_t), "scalars")
+            _contiguous(scalars=scalars)
             _on_device(scalars=scalars)
         a.scalars = _dptr(scalars)
         return a
@@ -214,6 +225,7 @@ def zero_tensors_norm(tensors: TensorSet, groups: Sequence[AdamGroup], step: int
     """The set's partial sums into slot `slot` of a zero_partials_bytes
     table, for zero_shard_combine."""
     _need(partials, (slot + 1) * lib().zero_partials_bytes(1), "partials")
+    _contiguous(partials=partials)
     _on_device(partials=partials)
     check(train_lib().zero_tensors_norm(ctypes.byref(tensors.args(groups, step, **hyper)), slot,
                                         _dptr(partials), _stream(stream)), "zero_tensors_norm")
@@ -223,6 +235,7 @@ def zero_tensors_apply(tensors: TensorSet, groups: Sequence[AdamGroup], step: in
                        stream=None, **hyper) -> None:
     """The update by a zero_global_t in device memory."""
     _need(global_buf, ctypes.sizeof(zero_global_t), "global_buf")
+    _contiguous(global_buf=global_buf)
     _on_device(global_buf=global_buf)
     check(train_lib().zero_tensors_apply(ctypes.byref(tensors.args(groups, step, **hyper)),
                                          _dptr(global_buf), _stream(stream)), "zero_tensors_apply")
@@ -292,6 +305,7 @@ class XentArgs:
             _need(m, 4 * t, name)
         _need(self.target, 8 * t, "target")
         _need(self.result, ctypes.sizeof(zero_xent_result_t), "result")
+        _contiguous(result=self.result, workspace=self.workspace)
         _on_device(x=x, w=w, target=self.target, loss=self.loss, lse=self.lse, result=self.result,
                    workspace=self.workspace, dx=self.dx if backward else None, dw=self.dw if backward else None)
         a.target, a.loss, a.lse = _dptr(self.target), _dptr(self.loss), _dptr(self.lse)
