@@ -99,3 +99,23 @@ def test_calls_refuse_buffers_that_are_not_contiguous(anywhere):
         Z.zero_tensors_apply(ts, groups, 1, strided(32, torch.uint8), stream=0)
     with pytest.raises(ValueError, match="scalars is not contiguous"):
         Z.zero_tensors_scalars(ts, groups, 1, scalars=byte.expand(288))
+
+
+class Elsewhere:
+    """What a check of devices sees of a tensor."""
+    is_cuda = True
+
+    def __init__(self, index):
+        self.device = torch.device("cuda", index)
+
+
+def test_calls_refuse_tensors_of_two_devices(monkeypatch):
+    train._on_device(a=Elsewhere(1), b=None, c=Elsewhere(1))
+    with pytest.raises(ValueError, match="b is on cuda:1, a on cuda:0"):
+        train._on_device(a=Elsewhere(0), b=Elsewhere(1))
+    # a set's tensors are checked against the first one's device
+    seen = []
+    monkeypatch.setattr(train, "_on_device", lambda **tensors: seen.append(tensors))
+    m, g = torch.zeros(300), torch.zeros(300, dtype=torch.bfloat16)
+    Z.TensorSet(master=[m, m.clone()], grad=[g, g], exp_avg=[m, m], exp_avg_sq=[m, m])
+    assert all(next(iter(t.values())) is m for t in seen) and len(seen) == 2

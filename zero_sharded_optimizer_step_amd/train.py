@@ -21,10 +21,18 @@ from ._train_abi import (ZERO_MAX_GROUPS, ZERO_STATE8_BLOCK, train_lib, zero_ada
 
 
 def _on_device(**tensors) -> None:
-    """Refuse host tensors: their addresses would fault the GPU."""
+    """Refuse host tensors and tensors of two devices: an address that the
+    launching GPU does not hold would fault it."""
+    first = None
     for name, t in tensors.items():
-        if t is not None and not t.is_cuda:
+        if t is None:
+            continue
+        if not t.is_cuda:
             raise ValueError("%s is on %s; expected device memory" % (name, t.device))
+        if first is None:
+            first = name
+        elif t.device != tensors[first].device:
+            raise ValueError("%s is on %s, %s on %s" % (name, t.device, first, tensors[first].device))
 
 
 def _contiguous(**tensors) -> None:
@@ -159,8 +167,9 @@ class TensorSet:
                 _need_state8(first[t], second[t], numel)
             if param is not None:
                 _need(param[t], 2 * numel, "param[%d]" % t)
-            _on_device(master=master[t], grad=grad[t], exp_avg=first[t], exp_avg_sq=second[t],
-                       param=param[t] if param is not None else None)
+            _on_device(**{"master[0]": master[0], "master[%d]" % t: master[t], "grad[%d]" % t: grad[t],
+                          "first state[%d]" % t: first[t], "second state[%d]" % t: second[t],
+                          "param[%d]" % t: param[t] if param is not None else None})
             recs.append(zero_tensor_t(_dptr(grad[t]), _dptr(master[t]), _dptr(first[t]), _dptr(second[t]),
                                       _dptr(param[t]) if param is not None else None, numel, group[t], 0))
         # tensors of the set's own on the same memory: the caller's lists may change
@@ -203,7 +212,7 @@ class TensorSet:
         if scalars is not None:
             _need(scalars, ctypes.sizeof(zero_tensors_scalars_t), "scalars")
             _contiguous(scalars=scalars)
-            _on_device(scalars=scalars)
+            _on_device(**{"scalars": scalars, "the set": self.result})
         a.scalars = _dptr(scalars)
         return a
 
@@ -226,7 +235,7 @@ def zero_tensors_norm(tensors: TensorSet, groups: Sequence[AdamGroup], step: int
     table, for zero_shard_combine."""
     _need(partials, (slot + 1) * lib().zero_partials_bytes(1), "partials")
     _contiguous(partials=partials)
-    _on_device(partials=partials)
+    _on_device(**{"partials": partials, "the set": tensors.result})
     check(train_lib().zero_tensors_norm(ctypes.byref(tensors.args(groups, step, **hyper)), slot,
                                         _dptr(partials), _stream(stream)), "zero_tensors_norm")
 
@@ -236,7 +245,7 @@ def zero_tensors_apply(tensors: TensorSet, groups: Sequence[AdamGroup], step: in
     """The update by a zero_global_t in device memory."""
     _need(global_buf, ctypes.sizeof(zero_global_t), "global_buf")
     _contiguous(global_buf=global_buf)
-    _on_device(global_buf=global_buf)
+    _on_device(**{"global_buf": global_buf, "the set": tensors.result})
     check(train_lib().zero_tensors_apply(ctypes.byref(tensors.args(groups, step, **hyper)),
                                          _dptr(global_buf), _stream(stream)), "zero_tensors_apply")
 
