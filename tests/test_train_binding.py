@@ -119,3 +119,41 @@ def test_calls_refuse_tensors_of_two_devices(monkeypatch):
     m, g = torch.zeros(300), torch.zeros(300, dtype=torch.bfloat16)
     Z.TensorSet(master=[m, m.clone()], grad=[g, g], exp_avg=[m, m], exp_avg_sq=[m, m])
     assert all(next(iter(t.values())) is m for t in seen) and len(seen) == 2
+
+
+class Recorded:
+    """A buffer that says which streams it was told of."""
+
+    def __init__(self, t):
+        self.t, self.streams = t, []
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+def test_a_sets_own_buffers_outlive_their_use_on_another_stream(anywhere, monkeypatch):
+    ts, groups = a_set(), [Z.AdamGroup()]
+    own = [Recorded(t) for t in (ts.table, ts.workspace, ts.result)]
+    ts.table, ts.workspace, ts.result = own
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: calls.append((name, a[-1])) or 0
+    monkeypatch.setattr(train, "train_lib", Lib)
+    table = torch.zeros(Z.zero_partials_bytes(1), dtype=torch.uint8)
+    a, b, c = Stream(5), Stream(6), Stream(7)
+    Z.zero_tensors_step(ts, groups, 1, stream=a)
+    Z.zero_tensors_step(ts, groups, 2, stream=a)
+    Z.zero_tensors_norm(ts, groups, 1, 0, table, stream=b)
+    Z.zero_tensors_apply(ts, groups, 1, torch.zeros(32, dtype=torch.uint8), stream=c)
+    assert [h for _, h in calls] == [5, 5, 6, 7]
+    assert all(q.streams == [a, b, c] for q in own)

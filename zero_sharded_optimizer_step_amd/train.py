@@ -128,7 +128,8 @@ class TensorSet:
     whatever becomes of the lists and tensors given here, and a tensor that
     moves or is replaced (a gradient in new memory, say) needs a new set.
     It owns the table, the workspace and `result`, the device zero_global_t
-    of the last step (32 bytes)."""
+    of the last step (32 bytes); calls on any stream may use them, one call
+    after another."""
 
     def __init__(self, master, grad, exp_avg=None, exp_avg_sq=None, state8=None, scale8=None,
                  param=None, group: Optional[Sequence[int]] = None):
@@ -182,6 +183,12 @@ class TensorSet:
         self.table = torch.frombuffer(table, dtype=torch.uint8).to(device)
         self.workspace = torch.empty(self.plan.workspace_bytes, dtype=torch.uint8, device=device)
         self.result = torch.zeros(32, dtype=torch.uint8, device=device)
+        self._streams = set()                            # handles that may use the three at once
+        if device.type == "cuda":
+            # ready for a step on any stream: the fill is done, and so is what
+            # used this memory before on the stream that it was allocated on
+            torch.cuda.current_stream(device).synchronize()
+            self._streams.add(torch.cuda.current_stream(device).cuda_stream)
         self._group_values = None
         a = self._c = zero_tensors_args()
         a.plan = self.plan
@@ -216,6 +223,21 @@ class TensorSet:
         a.scalars = _dptr(scalars)
         return a
 
+    def queue(self, stream=None) -> Optional[int]:
+        """The handle of `stream` (default: the current one); the set's own
+        buffers outlive what a call queues there."""
+        handle = _stream(stream)
+        if handle not in self._streams:
+            torch = _torch()
+            if stream is None:
+                stream = torch.cuda.current_stream()
+            elif isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream)
+            for t in (self.table, self.workspace, self.result):
+                t.record_stream(stream)
+            self._streams.add(handle)
+        return handle
+
 
 def zero_tensors_step(tensors: TensorSet, groups: Sequence[AdamGroup], step: int,
                       want_info: bool = False, stream=None, **hyper) -> Optional[zero_global_t]:
@@ -225,7 +247,7 @@ def zero_tensors_step(tensors: TensorSet, groups: Sequence[AdamGroup], step: int
     a = tensors.args(groups, step, **hyper)
     info = zero_global_t() if want_info else None
     check(train_lib().zero_tensors_step(ctypes.byref(a), ctypes.byref(info) if want_info else None,
-                                        _stream(stream)), "zero_tensors_step")
+                                        tensors.queue(stream)), "zero_tensors_step")
     return info
 
 
@@ -237,7 +259,7 @@ def zero_tensors_norm(tensors: TensorSet, groups: Sequence[AdamGroup], step: int
     _contiguous(partials=partials)
     _on_device(**{"partials": partials, "the set": tensors.result})
     check(train_lib().zero_tensors_norm(ctypes.byref(tensors.args(groups, step, **hyper)), slot,
-                                        _dptr(partials), _stream(stream)), "zero_tensors_norm")
+                                        _dptr(partials), tensors.queue(stream)), "zero_tensors_norm")
 
 
 def zero_tensors_apply(tensors: TensorSet, groups: Sequence[AdamGroup], step: int, global_buf,
@@ -247,7 +269,7 @@ def zero_tensors_apply(tensors: TensorSet, groups: Sequence[AdamGroup], step: in
     _contiguous(global_buf=global_buf)
     _on_device(**{"global_buf": global_buf, "the set": tensors.result})
     check(train_lib().zero_tensors_apply(ctypes.byref(tensors.args(groups, step, **hyper)),
-                                         _dptr(global_buf), _stream(stream)), "zero_tensors_apply")
+                                         _dptr(global_buf), tensors.queue(stream)), "zero_tensors_apply")
 
 
 def zero_tensors_scalars(tensors: TensorSet, groups: Sequence[AdamGroup], step: int,
