@@ -35,9 +35,11 @@ int tensors_constants(const zero_tensors_args* a, bool peers, bool buffers, zero
     const zero_tensors_plan_t& p = a->plan;
     int rc;
     if ((rc = check_plan_types(p.state_bits, p.grad_dtype, p.param_dtype))) return rc;
-    // the first two bound the third and fourth, so nothing overflows
+    // the size and the count of chunks bound each other, and a chunk is one
+    // tensor's and holds an element; nothing here overflows
     if (p.n_tensors < 0 || p.numel < 0 || p.n_chunks < 0 || p.n_chunks > INT32_MAX ||
-        p.n_chunks < (p.numel + kChunk - 1) / kChunk ||
+        p.numel > static_cast<int64_t>(INT32_MAX) * kChunk || (p.n_tensors == 0 && p.n_chunks > 0) ||
+        p.n_chunks > p.numel || p.n_chunks < (p.numel + kChunk - 1) / kChunk ||
         p.n_chunks > p.numel / kChunk + p.n_tensors || p.n_groups < 1 ||
         p.n_groups > ZERO_MAX_GROUPS ||
         p.table_bytes != round_up(table_map_offset(p.n_tensors) + 4u * static_cast<size_t>(p.n_chunks), 16) ||
