@@ -1203,7 +1203,9 @@ int backward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
             e.c = reinterpret_cast<char*>(dw_slab);
             e.ldc = c.dim_pad;
             e.slab = c.piece * c.dim_pad;
-            launch_product<DT, kCols, kCols, kSlab>(e, c.dw_slices, st);
+            // more than one slice only where tiles times slices are at most 512
+            // of 128 x 128, one round of the chip: large_tiles is false
+            launch_tiles<DT, kCols, kCols, kSlab, 128, 128, 2, 2>(e, c.dw_slices, st);
             hipLaunchKernelGGL((slab_sum_kernel<DT>),
                                dim3(blocks_for(rows * (c.dim_pad / 4))), dim3(256), 0, st,
                                dw_slab, c.dw_slices, e.slab, rows, a->dim, c.dim_pad, a->result, grad, nullptr,
