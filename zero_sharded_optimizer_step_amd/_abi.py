@@ -168,6 +168,13 @@ def lib() -> ctypes.CDLL:
             raise ImportError(
                 "libzero_mi355x.so is not built (expected at %s); run "
                 "`python -m zero_sharded_optimizer_step_amd.build`" % LIB_PATH)
+        # torch brings a HIP runtime of its own.  Loaded first, it is the one
+        # that the library links to; loaded after, the process has two and the
+        # library's launches find no device.
+        try:
+            import torch  # noqa: F401
+        except ImportError:
+            pass                                         # the host calls need none
         L = ctypes.CDLL(LIB_PATH)
         for name, (res, args) in _PROTOTYPES.items():
             fn = getattr(L, name)
