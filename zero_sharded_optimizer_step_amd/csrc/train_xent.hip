@@ -1029,14 +1029,25 @@ void launch_tiles(Product q, int slices, hipStream_t st) {
 int64_t tiles_of(const Product& q, int64_t bm, int64_t bn) { return up(q.m, bm) / bm * (up(q.n, bn) / bn); }
 
 // 256 x 256 or 128 x 128: by how often each fills the chip, the larger one
-// block a CU, the smaller two, a round of the larger taking 1.6 times one of
-// the smaller.  Forward of 2048 tokens x 4096, 128 x 128 and 256 x 256: 4096
-// of the vocabulary (128 large tiles) 68 and 87 us, 5120 (160) 103 and 86,
-// 8192 (256) 124 and 103, 8448 (264) 153 and 174, 16384 (512) 238 and 196.
+// block a CU, the smaller two.  Microseconds for 128 x 128 and 256 x 256, bf16:
+//   - of 1024 of k or more a round of the larger takes 1.6 times one of the
+//     smaller, and a round takes its time however few blocks are in it.
+//     Forward of 2048 tokens x 4096: 4096 of the vocabulary (128 large tiles)
+//     68 and 87, 5120 (160) 103 and 86, 8192 (256) 124 and 103, 8448 (264) 153
+//     and 174, 16384 (512) 238 and 196;
+//   - of less, 1.8 times, and the smaller's last round takes its share only:
+//     a block alone on its CU is the faster, and so it is with few steps
+//     between a tile's start and its epilogue.  Forward of 2048 x 256 x 6016
+//     12.8 and 17.1, 4096 x 512 x 10007 45 and 53, x 32000 150 and 134; dw of
+//     509 tokens x 1000 x 10007 18.6 and 20.6, x 16384 23.2 and 22.7.
+// Against the better of the two each time, over 64 to 4096 of k, this loses
+// 0.4 % on average (648 forwards and Ps, 270 dws, the worst 25 %: 14.0 us for
+// 11.2); the first half alone would lose 1.6 %.
 bool large_tiles(const Product& q, int slices) {
+    const int64_t small = tiles_of(q, 128, 128) * slices;
     const int64_t large = (tiles_of(q, 256, 256) * slices + kCus - 1) / kCus;
-    const int64_t small = (tiles_of(q, 128, 128) * slices + 2 * kCus - 1) / (2 * kCus);
-    return 8 * large <= 5 * small;
+    if (q.slice < 1024) return 9 * large * (2 * kCus) <= 5 * small;
+    return 8 * large <= 5 * ((small + 2 * kCus - 1) / (2 * kCus));
 }
 
 template <int DT, Layout LA, Layout LB, Epilogue E>
