@@ -37,13 +37,18 @@ extern "C" {
  *   e = 0:  (f/8)     * 2^(1 - B + E - 127)      (gradual underflow)
  * A second moment above zero never takes code 0, so that no update divides
  * by eps alone because of the rounding.  A magnitude past the top code
- * (an infinite second moment) takes the top code.
+ * (an infinite second moment) takes the top code: the format has no infinity
+ * and no NaN.  Either moves its block to E = 254, under which a first moment
+ * below 2^109 becomes 0 and a second moment below 2^94 becomes 2^94.
  */
 #define ZERO_STATE8_BLOCK 256
 
 /* m[0, n) and v[0, n) (fp32, device, 16-byte aligned; v >= 0) into n8 =
  * ceil(n / 256) blocks: state8 (512 n8 bytes, 16-byte aligned) and scale8
- * (2 n8 bytes, 2-byte aligned), rounded to nearest even.
+ * (2 n8 bytes, 2-byte aligned), rounded to nearest even.  Moments that hold
+ * NaN are not detected: a NaN in m, or one without its sign bit in v, is
+ * held as an infinity is, one with it in v as 0.  zero_tensors_step writes
+ * none (a gradient that is not finite skips the step).
  * Errors: n < 0, a NULL pointer when n > 0 -> ZERO_EINVAL; misalignment ->
  * ZERO_EALIGN; launch -> ZERO_EDEVICE. */
 int zero_state8_encode(const float* m, const float* v, int64_t n, void* state8, void* scale8,
@@ -192,7 +197,8 @@ int zero_tensors_scalars(const zero_tensors_args* a, zero_tensors_scalars_t* out
  * order.  P is rounded to 16 bits for the two products of the gradient
  * (a relative half step of the dtype, what dx and dw are rounded by too).
  * Results do not depend on timing.  A row whose logits are all -inf has
- * lse = -inf; +inf or NaN logits give an infinite or NaN lse.
+ * lse = -inf; +inf or NaN logits give an infinite or NaN lse; any finite
+ * logits, the type's lowest value among them, a finite lse.
  */
 typedef struct {
     double  loss_sum;

@@ -244,8 +244,8 @@ __device__ __forceinline__ bool infinite(float x) { return __builtin_fabsf(x) ==
 
 // The product's tile by tile.  What bounds a large one is the matrix cores'
 // power: at 4096 tokens x 4096 x 128000 in bf16 the clock falls to 1.85 GHz,
-// and the forward takes 2.95 to 3.0 ms (1.44 PFLOP/s) with values of a normal
-// distribution and 2.51 ms with zeros.  Hence
+// and the forward takes 2.87 to 3.0 ms (1.43 to 1.5 PFLOP/s) with values of a
+// normal distribution and 2.51 ms with zeros.  Hence
 //   - four waves with 128 x 128 of a 256 x 256 tile each, one a SIMD, so that
 //     a value out of LDS serves 8 products of 16 x 16 x 32 (eight waves of
 //     128 x 64 read half as much again: 3.35 ms with all of the below lacking);
@@ -476,6 +476,11 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
             };
             split(column);
         } else if constexpr (E == kProb) {
+            // In 16 bits, as the matrix cores of the two products take it: half
+            // a step each, independent, beside the half step that dx and dw are
+            // rounded by at the end.  Errors of the gradients against 64 bits
+            // (relative, all of them): bf16, 4096 x 4096 x 128000 1.7e-3, with P
+            // in fp32 1.7e-3; fp16, 509 x 1000 x 10007 2.2e-4 and 2.1e-4.
             const float bias = q.scale > 1.0f ? 15.0f : 0.0f;      // log2 of the scale
             auto column = [&](auto edge, auto index) __attribute__((always_inline)) -> void {
                 constexpr int j = decltype(index)::value;
@@ -600,10 +605,10 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
 // kLse of up to 8 tokens: w is read once and nothing else counts, so the
 // fragments go from memory to registers, many loads at a time.  A block takes
 // 16 rows of w; its four waves take every fourth 64 of k, and the sums meet
-// in LDS in a fixed order.  Whole forward at dim 4096 in bf16 and that of the
-// 128 x 128 tiles: 1 token x 32000 54 us (4.9 TB/s) and 64, 1 x 128000 180 us
-// (5.8 TB/s) and 203, 8 x 32000 65 and 72, but 16 x 32000 89 and 78, since
-// every block reads x again.
+// in LDS in a fixed order.  Whole forward at dim 4096 in bf16, w from memory,
+// and that of the 128 x 128 tiles: 1 token x 32000 51.8 us (5.1 TB/s) and 67.9,
+// 1 x 128000 176 us (6.0 TB/s) and 204, 4 x 32000 54.7 and 68.7, 8 62.3 and
+// 67.7, 12 69.7 and 69.4, but 16 85.9 and 71.0, since every block reads x again.
 template <int DT>
 __global__ __launch_bounds__(256) void few_kernel(const Product q) {
     constexpr int kGroup = 2;                              // of 64 k a wave and turn
@@ -731,9 +736,9 @@ __global__ __launch_bounds__(1024) void xent_rows_kernel(const f32x2* __restrict
     }
 }
 
-// Up to 16 tokens: one block joins the slots of all of them and the mean, so
-// that scoring a token takes two launches: one token x 4096 x 32000 in bf16,
-// with w in the last-level cache, takes 41 us, with three launches 67.
+// Up to kFewTokens tokens (it has room for 16): one block joins the slots of
+// all of them and the mean in 4.1 us, where the two kernels above and below
+// take 4.7 and 3.9 and the gap between them.
 __global__ __launch_bounds__(1024) void xent_few_kernel(const f32x2* __restrict__ partial, int slots, int tokens,
                                                         const float* __restrict__ target_logit,
                                                         const int64_t* __restrict__ target, int64_t vocab,

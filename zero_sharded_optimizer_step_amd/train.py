@@ -129,7 +129,9 @@ class TensorSet:
     moves or is replaced (a gradient in new memory, say) needs a new set.
     It owns the table, the workspace and `result`, the device zero_global_t
     of the last step (32 bytes); calls on any stream may use them, one call
-    after another."""
+    after another.  All of a set's calls share these and one argument record:
+    steps of one set that overlap, on two streams or from two threads,
+    overwrite each other's partials and constants."""
 
     def __init__(self, master, grad, exp_avg=None, exp_avg_sq=None, state8=None, scale8=None,
                  param=None, group: Optional[Sequence[int]] = None):
@@ -200,7 +202,8 @@ class TensorSet:
     def args(self, groups: Sequence[AdamGroup], step: int, loss_scale: float = 1.0,
              max_grad_norm: float = 1.0, seed: int = 0, grad_predivide: float = 1.0,
              peer_sumsq: float = 0.0, peer_overflow: bool = False, scalars=None) -> zero_tensors_args:
-        """The zero_tensors_args of a call; `scalars` is a device copy of a
+        """The zero_tensors_args of a call, the set's one record: it holds
+        until the next call.  `scalars` is a device copy of a
         zero_tensors_scalars_t (288 bytes) or None."""
         a = self._c
         values = [(g.lr, g.beta1, g.beta2, g.eps, g.weight_decay) for g in groups]
