@@ -117,8 +117,11 @@ def test_calls_refuse_tensors_of_two_devices(monkeypatch):
     seen = []
     monkeypatch.setattr(train, "_on_device", lambda **tensors: seen.append(tensors))
     m, g = torch.zeros(300), torch.zeros(300, dtype=torch.bfloat16)
-    Z.TensorSet(master=[m, m.clone()], grad=[g, g], exp_avg=[m, m], exp_avg_sq=[m, m])
-    assert all(next(iter(t.values())) is m for t in seen) and len(seen) == 2
+    away = torch.zeros(300, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(Z.ZeroError):                     # it has no address
+        Z.TensorSet(master=[m, m.clone()], grad=[g, away], exp_avg=[m, m], exp_avg_sq=[m, m])
+    assert [list(t) for t in seen] == [["master[0]", "grad[1]"], ["master[0]"]]
+    assert seen[0]["grad[1]"] is away
 
 
 class Recorded:

@@ -151,6 +151,7 @@ class TensorSet:
         param_dtype = param[0].dtype if param is not None and n else None
         state_dtype = torch.float32 if bits == 32 else torch.uint8
         recs = []
+        device = master[0].device if n else torch.device("cuda")
         for t in range(n):
             numel = master[t].numel()
             for what, x, dtype in (("master", master[t], torch.float32), ("grad", grad[t], grad_dtype),
@@ -162,6 +163,8 @@ class TensorSet:
                     raise ValueError("tensor %d: %s is %s, expected %s" % (t, what, x.dtype, dtype))
                 if not x.is_contiguous():
                     raise ValueError("tensor %d: %s is not contiguous" % (t, what))
+                if x.device != device:
+                    _on_device(**{"master[0]": master[0], "%s[%d]" % (what, t): x})
             _need(grad[t], grad[t].element_size() * numel, "grad[%d]" % t)
             if bits == 32:
                 _need(first[t], 4 * numel, "exp_avg[%d]" % t)
@@ -170,18 +173,16 @@ class TensorSet:
                 _need_state8(first[t], second[t], numel)
             if param is not None:
                 _need(param[t], 2 * numel, "param[%d]" % t)
-            _on_device(**{"master[0]": master[0], "master[%d]" % t: master[t], "grad[%d]" % t: grad[t],
-                          "first state[%d]" % t: first[t], "second state[%d]" % t: second[t],
-                          "param[%d]" % t: param[t] if param is not None else None})
             recs.append(zero_tensor_t(_dptr(grad[t]), _dptr(master[t]), _dptr(first[t]), _dptr(second[t]),
                                       _dptr(param[t]) if param is not None else None, numel, group[t], 0))
-        # tensors of the set's own on the same memory: the caller's lists may change
-        self._keep = [x.detach() for seq in (master, grad, first, second, param) if seq is not None
+        if n:
+            _on_device(**{"master[0]": master[0]})       # and with it all others
+        # the memory itself: the caller's lists may change, and what lies behind a tensor
+        self._keep = [x.untyped_storage() for seq in (master, grad, first, second, param) if seq is not None
                       for x in seq if x is not None]
         self.state_bits = bits
         self.plan, table = zero_tensors_plan(recs, bits, grad_dtype,
                                              0 if param_dtype is None else dtype_code(param_dtype))
-        device = master[0].device if n else torch.device("cuda")
         self.table = torch.frombuffer(table, dtype=torch.uint8).to(device)
         self.workspace = torch.empty(self.plan.workspace_bytes, dtype=torch.uint8, device=device)
         self.result = torch.zeros(32, dtype=torch.uint8, device=device)
