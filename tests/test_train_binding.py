@@ -160,3 +160,40 @@ def test_a_sets_own_buffers_outlive_their_use_on_another_stream(anywhere, monkey
     Z.zero_tensors_apply(ts, groups, 1, torch.zeros(32, dtype=torch.uint8), stream=c)
     assert [h for _, h in calls] == [5, 5, 6, 7]
     assert all(q.streams == [a, b, c] for q in own)
+
+
+def test_calls_refuse_another_device_than_the_current_one(anywhere, monkeypatch):
+    # a call launches on the current device, with that device's stream
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    ts, groups = a_set(), [Z.AdamGroup()]
+    launched = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: launched.append(name) or 0
+    monkeypatch.setattr(train, "train_lib", Lib)
+    table = torch.zeros(Z.zero_partials_bytes(1), dtype=torch.uint8)
+    own = [Recorded(t) for t in (ts.table, ts.workspace, ts.result)]
+    ts.table, ts.workspace, ts.result = own
+    monkeypatch.setattr(train.XentArgs, "c_args", lambda self, backward: train.zero_xent_args())
+    xent = Z.XentArgs(*[own[2]] * 7)
+    m, s8, e8 = torch.zeros(300), torch.zeros(1024, dtype=torch.uint8), torch.zeros(4, dtype=torch.uint8)
+    state = Recorded(m)
+    calls = [lambda: Z.zero_tensors_step(ts, groups, 1, stream=0),
+             lambda: Z.zero_tensors_norm(ts, groups, 1, 0, table, stream=0),
+             lambda: Z.zero_tensors_apply(ts, groups, 1, torch.zeros(32, dtype=torch.uint8), stream=0),
+             lambda: Z.zero_xent_forward(xent, stream=0), lambda: Z.zero_xent_backward(xent, stream=0),
+             lambda: Z.zero_state8_encode(state, m, s8, e8, stream=0),
+             lambda: Z.zero_state8_decode(s8, e8, state, m, stream=0)]
+    for t in (own[2], state):
+        t.is_cuda, t.device = True, torch.device("cuda", 1)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: Stream(handle))
+    for call in calls:
+        with pytest.raises(ValueError, match="on cuda:1; the current device is cuda:0"):
+            call()
+    assert not launched
+    for t in (own[2], state):
+        t.device = torch.device("cuda", 0)
+    for call in calls:
+        call()
+    assert len(launched) == len(calls)

@@ -22,7 +22,7 @@ from ._train_abi import (ZERO_MAX_GROUPS, ZERO_STATE8_BLOCK, train_lib, zero_ada
 
 def _on_device(**tensors) -> None:
     """Refuse host tensors and tensors of two devices: an address that the
-    launching GPU does not hold would fault it."""
+    launching GPU does not hold would fault it (see _launching)."""
     first = None
     for name, t in tensors.items():
         if t is None:
@@ -33,6 +33,14 @@ def _on_device(**tensors) -> None:
             first = name
         elif t.device != tensors[first].device:
             raise ValueError("%s is on %s, %s on %s" % (name, t.device, first, tensors[first].device))
+
+
+def _launching(t) -> None:
+    """Refuse tensors of another device than the current one, on which a call
+    launches its kernels."""
+    if t.is_cuda and t.device.index != _torch().cuda.current_device():
+        raise ValueError("the tensors are on %s; the current device is cuda:%d"
+                         % (t.device, _torch().cuda.current_device()))
 
 
 def _contiguous(**tensors) -> None:
@@ -66,6 +74,7 @@ def zero_state8_encode(exp_avg, exp_avg_sq, state8, scale8, n: Optional[int] = N
     _need_state8(state8, scale8, n)
     _contiguous(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, state8=state8, scale8=scale8)
     _on_device(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, state8=state8, scale8=scale8)
+    _launching(exp_avg)
     check(train_lib().zero_state8_encode(_dptr(exp_avg), _dptr(exp_avg_sq), n, _dptr(state8),
                                          _dptr(scale8), _stream(stream)), "zero_state8_encode")
 
@@ -82,6 +91,7 @@ def zero_state8_decode(state8, scale8, exp_avg, exp_avg_sq, n: Optional[int] = N
     _need_state8(state8, scale8, n)
     _contiguous(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, state8=state8, scale8=scale8)
     _on_device(exp_avg=exp_avg, exp_avg_sq=exp_avg_sq, state8=state8, scale8=scale8)
+    _launching(exp_avg)
     check(train_lib().zero_state8_decode(_dptr(state8), _dptr(scale8), n, _dptr(exp_avg),
                                          _dptr(exp_avg_sq), dtype_code(exp_avg.dtype), _stream(stream)),
           "zero_state8_decode")
@@ -230,6 +240,7 @@ class TensorSet:
     def queue(self, stream=None) -> Optional[int]:
         """The handle of `stream` (default: the current one); the set's own
         buffers outlive what a call queues there."""
+        _launching(self.result)
         handle = _stream(stream)
         if handle not in self._streams:
             torch = _torch()
@@ -353,11 +364,15 @@ class XentArgs:
 
 def zero_xent_forward(args: XentArgs, stream=None) -> None:
     """loss, lse and result of args."""
-    check(train_lib().zero_xent_forward(ctypes.byref(args.c_args(False)), _stream(stream)),
+    a = args.c_args(False)
+    _launching(args.x)
+    check(train_lib().zero_xent_forward(ctypes.byref(a), _stream(stream)),
           "zero_xent_forward")
 
 
 def zero_xent_backward(args: XentArgs, stream=None) -> None:
     """dx and dw of args, after zero_xent_forward of the same args."""
-    check(train_lib().zero_xent_backward(ctypes.byref(args.c_args(True)), _stream(stream)),
+    a = args.c_args(True)
+    _launching(args.x)
+    check(train_lib().zero_xent_backward(ctypes.byref(a), _stream(stream)),
           "zero_xent_backward")
