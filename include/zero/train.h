@@ -1,8 +1,9 @@
 /*
  * zero/train.h -- C ABI of the training operators that sit next to the ZeRO
  * shard step: AdamW over a list of tensors with 32-bit or 8-bit states, the
- * conversion between the two states, and the softmax cross entropy of a
- * large vocabulary with its gradient.
+ * conversion between the two states, the softmax cross entropy of a large
+ * vocabulary with its gradient, and activations held in 8 bits with what
+ * reads them: a gated activation and a product, each with its gradient.
  *
  * libzero_train_mi355x.so holds them; it uses libzero_mi355x.so (errors,
  * the step's constants).  The conventions are those of zero.h: ZERO_OK or a
@@ -242,6 +243,154 @@ int zero_xent_forward(const zero_xent_args* a, void* stream);
 /* Writes dx and dw from x, w, target and the forward's lse and *result;
  * loss is not used.  Errors as above. */
 int zero_xent_backward(const zero_xent_args* a, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rows of 8-bit codes: an activation kept for the backward (a row is a
+ * token), or a weight (a row is an output channel).
+ *
+ * A row is held as whole numbers q of [-127, 127] and one fp32 scale s, and
+ * stands for q s.  The encoder takes s = 2^e with the smallest e under which
+ * the row's largest magnitude rounds to 127 or less, e clamped to [-24, 9]
+ * for fp16 and [-126, 121] for bf16 and fp32, and q = row / s to nearest
+ * even, clamped.  A power of two makes every q s a value of the row's own
+ * 16-bit type: nothing that reads the row in 16 bits rounds it again, and
+ * the codes depend on the row alone.  A row that holds an infinity or a NaN
+ * has a NaN scale (and codes 0): all of it reads as NaN, so that the
+ * overflow reaches the gradients and the step's flag.
+ *
+ * A row of codes takes ZERO_ROWS8_BYTES(dim) bytes, dim rounded up to a
+ * multiple of 16, and holds zeros from dim on; the encoder writes them.
+ * Whoever makes codes by other means writes them too.  Rows start at
+ * multiples of 16 bytes: 16-byte aligned, strides multiples of 16.  What
+ * lies between a row's ZERO_ROWS8_BYTES and the next row is neither read nor
+ * written.  The readers below take codes of [-128, 127] and any fp32 scale
+ * as they are.
+ */
+#define ZERO_ROWS8_MAX_DIM 131071
+#define ZERO_ROWS8_BYTES(dim) (((dim) + 15) / 16 * 16)
+
+/* x: rows x dim values of dtype ZERO_FP16, ZERO_BF16 or ZERO_FP32, aligned to
+ * its element, x_stride (elements, >= dim, <= 2^31) from row to row.
+ * rows in [0, 2^31), dim in [0, ZERO_ROWS8_MAX_DIM]; a row of no elements or
+ * of zeros has the least scale.
+ * Errors: a size, stride or dtype out of range, a NULL pointer where there is
+ * something to read or write -> ZERO_EINVAL; misalignment -> ZERO_EALIGN;
+ * launch -> ZERO_EDEVICE. */
+int zero_rows8_encode(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, int64_t dim,
+                      void* codes, int64_t codes_stride, float* scale, void* stream);
+
+/* The reverse: y = q s in fp32, rounded to nearest even to dtype. */
+int zero_rows8_decode(const void* codes, int64_t codes_stride, const float* scale, int64_t rows,
+                      int64_t dim, void* y, int64_t y_stride, int32_t dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The gated activation with its input kept in 8 bits.
+ *
+ *   forward    h = act(gate) up,  or act(gate) where up is NULL,
+ *              in fp32, rounded to dtype; gate and up into gate8 and up8 as
+ *              zero_rows8_encode does, and h into h8 (the rounded h, as
+ *              zero_rows8_encode would find it), in one pass
+ *   backward   dgate = dh up^ act'(gate^),  dup = dh act(gate^)
+ *              of the values gate^ and up^ that the codes stand for
+ *
+ *   ZERO_GLU_SILU  act(x) = x p, p = 1 / (1 + exp(-x))
+ *   ZERO_GLU_GELU  act(x) = x p, p = 1 / (1 + exp(-2 sqrt(2/pi) (x + 0.044715 x^3)))
+ *                  (the tanh form of gelu: p = (1 + tanh(..)) / 2)
+ *
+ * Results depend on the inputs alone.  A token whose gate or up holds an
+ * infinity or a NaN has NaN in all of the gradients that read that row of
+ * codes; so has, in h8, one whose h overflowed.  Other tokens are not
+ * touched by it.
+ */
+#define ZERO_GLU_SILU 0
+#define ZERO_GLU_GELU 1
+
+typedef struct {
+    int64_t tokens, width;    /* [0, 2^31), [0, ZERO_ROWS8_MAX_DIM]             */
+    /* elements from row to row, >= width, <= 2^31; of codes bytes, multiples of
+     * 16, >= ZERO_ROWS8_BYTES(width), <= 2^31; of a buffer that is NULL unused */
+    int64_t gate_stride, up_stride, h_stride, dh_stride, dgate_stride, dup_stride;
+    int64_t gate8_stride, up8_stride, h8_stride;
+    int32_t dtype;            /* ZERO_FP16 or ZERO_BF16: gate, up, h, dh, dgate, dup */
+    int32_t kind;             /* ZERO_GLU_SILU or ZERO_GLU_GELU                 */
+    const void* gate;         /* device, 2-byte aligned                         */
+    const void* up;           /* or NULL                                        */
+    void* gate8;              /* out of the forward, in of the backward; NULL in
+                                 a forward that no backward follows             */
+    float* gate_scale;
+    void* up8;                /* as gate8; NULL where there is no up            */
+    float* up_scale;
+    void* h;                  /* out; NULL: not wanted in 16 bits               */
+    void* h8;                 /* out; NULL: not wanted in 8 bits                */
+    float* h_scale;
+    const void* dh;           /* in of the backward                             */
+    void* dgate;              /* out of the backward                            */
+    void* dup;                /* as dgate; NULL where there is no up8           */
+} zero_glu8_args;
+
+/* Writes h or h8 or both, and gate8 and up8 where they are given; dh, dgate
+ * and dup are not used.  No output may overlap an input or another output.
+ * No token, or a width of 0: nothing is written.
+ * Errors: NULL or out-of-range arguments -> ZERO_EINVAL; misalignment (2
+ * bytes for the 16-bit buffers, 16 for codes, 4 for scales) -> ZERO_EALIGN;
+ * launch -> ZERO_EDEVICE. */
+int zero_glu8_forward(const zero_glu8_args* a, void* stream);
+
+/* Writes dgate and dup from dh, gate8 and up8 with their scales; gate, up, h
+ * and h8 are not used.  dgate or dup may be dh itself, with its stride.
+ * Errors as above. */
+int zero_glu8_backward(const zero_glu8_args* a, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The product of 8-bit rows with 8-bit weights, and its gradient.
+ *
+ *   forward    y_tn = x_scale_t w_scale_n sum_k x8_tk w8_nk + bias_n
+ *   backward   dx = dy w^,  dw = dy^T x^,  db_n = sum_t dy_tn
+ *              of the values x^ = x8 x_scale and w^ = w8 w_scale
+ *
+ * x8: tokens rows of dim codes, w8: out rows of dim codes, each with its
+ * rows' scales.  The forward's sums are whole numbers in 32 bits, exact; one
+ * is scaled and the bias added in fp32 and rounded once.  The backward takes
+ * x^ and w^ in dtype (exact where the scales are the encoder's for rows of
+ * that dtype, else rounded to nearest even) times dy, with fp32 sums, and
+ * rounds once.  Results do not depend on timing.
+ */
+typedef struct {
+    int64_t tokens, dim, out; /* [0, 2^20], [0, ZERO_ROWS8_MAX_DIM], [0, 2^20]  */
+    int64_t x8_stride, w8_stride;     /* bytes, multiples of 16, >= ZERO_ROWS8_BYTES(dim),
+                                         <= 2^22                                */
+    int64_t y_stride, dy_stride;      /* elements, >= out, <= 2^31              */
+    int64_t dx_stride, dw_stride;     /* >= dim, <= 2^31                        */
+    int32_t dtype;            /* ZERO_FP16 or ZERO_BF16: y, bias, dy, dx, dw, db */
+    int32_t reserved;         /* 0                                              */
+    const void* x8;           /* device, 16-byte aligned                        */
+    const float* x_scale;     /* device fp32[tokens]                            */
+    const void* w8;
+    const float* w_scale;     /* device fp32[out]                               */
+    const void* bias;         /* device, out values, 2-byte aligned, or NULL    */
+    void* y;                  /* out of the forward, 2-byte aligned             */
+    const void* dy;           /* in of the backward, 2-byte aligned             */
+    void* dx;                 /* out of the backward; NULL: not wanted          */
+    void* dw;                 /* likewise                                       */
+    void* db;                 /* likewise                                       */
+    void* workspace;          /* device, 256-byte aligned                       */
+    size_t workspace_bytes;
+} zero_linear8_args;
+
+/* Bytes of workspace forward and backward need (one buffer serves both; no
+ * call reads what another left there).  0 for out-of-range sizes.  Host only. */
+size_t zero_linear8_workspace_bytes(int64_t tokens, int64_t dim, int64_t out);
+
+/* Writes y; dy, dx, dw and db are not used.  No output may overlap an input.
+ * Errors: NULL or out-of-range arguments -> ZERO_EINVAL; misalignment ->
+ * ZERO_EALIGN; workspace_bytes too small -> ZERO_ESIZE; launch ->
+ * ZERO_EDEVICE. */
+int zero_linear8_forward(const zero_linear8_args* a, void* stream);
+
+/* Writes those of dx, dw and db that are given from dy, w8 (dx) and x8 (dw)
+ * with their scales; bias and y are not used.  No token: dw and db are zero;
+ * no output channel: dx is zero.  Errors as above. */
+int zero_linear8_backward(const zero_linear8_args* a, void* stream);
 
 #ifdef __cplusplus
 }

@@ -13,6 +13,8 @@ TRAIN_LIB_PATH = os.path.join(_abi.PKG, "libzero_train_mi355x.so")
 
 ZERO_STATE8_BLOCK = 256
 ZERO_MAX_GROUPS = 8
+ZERO_ROWS8_MAX_DIM = 131071
+ZERO_GLU_SILU, ZERO_GLU_GELU = 0, 1
 u32, u64 = ctypes.c_uint32, ctypes.c_uint64
 
 
@@ -69,6 +71,23 @@ class zero_xent_args(ctypes.Structure):
                 ("workspace_bytes", sz)]
 
 
+class zero_glu8_args(ctypes.Structure):
+    _fields_ = [("tokens", i64), ("width", i64), ("gate_stride", i64), ("up_stride", i64),
+                ("h_stride", i64), ("dh_stride", i64), ("dgate_stride", i64), ("dup_stride", i64),
+                ("gate8_stride", i64), ("up8_stride", i64), ("h8_stride", i64), ("dtype", i32),
+                ("kind", i32), ("gate", vp), ("up", vp), ("gate8", vp), ("gate_scale", vp),
+                ("up8", vp), ("up_scale", vp), ("h", vp), ("h8", vp), ("h_scale", vp), ("dh", vp),
+                ("dgate", vp), ("dup", vp)]
+
+
+class zero_linear8_args(ctypes.Structure):
+    _fields_ = [("tokens", i64), ("dim", i64), ("out", i64), ("x8_stride", i64), ("w8_stride", i64),
+                ("y_stride", i64), ("dy_stride", i64), ("dx_stride", i64), ("dw_stride", i64),
+                ("dtype", i32), ("reserved", i32), ("x8", vp), ("x_scale", vp), ("w8", vp),
+                ("w_scale", vp), ("bias", vp), ("y", vp), ("dy", vp), ("dx", vp), ("dw", vp),
+                ("db", vp), ("workspace", vp), ("workspace_bytes", sz)]
+
+
 _P = ctypes.POINTER
 _PROTOTYPES = {
     "zero_state8_encode": (ctypes.c_int, [vp, vp, i64, vp, vp, vp]),
@@ -82,6 +101,13 @@ _PROTOTYPES = {
     "zero_xent_workspace_bytes": (sz, [i64, i64, i64]),
     "zero_xent_forward": (ctypes.c_int, [_P(zero_xent_args), vp]),
     "zero_xent_backward": (ctypes.c_int, [_P(zero_xent_args), vp]),
+    "zero_rows8_encode": (ctypes.c_int, [vp, i64, i32, i64, i64, vp, i64, vp, vp]),
+    "zero_rows8_decode": (ctypes.c_int, [vp, i64, vp, i64, i64, vp, i64, i32, vp]),
+    "zero_glu8_forward": (ctypes.c_int, [_P(zero_glu8_args), vp]),
+    "zero_glu8_backward": (ctypes.c_int, [_P(zero_glu8_args), vp]),
+    "zero_linear8_workspace_bytes": (sz, [i64, i64, i64]),
+    "zero_linear8_forward": (ctypes.c_int, [_P(zero_linear8_args), vp]),
+    "zero_linear8_backward": (ctypes.c_int, [_P(zero_linear8_args), vp]),
 }
 
 _lib = None

@@ -31,7 +31,8 @@ SOURCES = ["zero_host.cpp", "zero_offload.cpp", "zero_kernels.hip"]
 # stay valid when an operator changes.  It links to that library.
 TRAIN_LIB_NAME = "libzero_train_mi355x.so"
 TRAIN_LIB_PATH = os.path.join(PKG, TRAIN_LIB_NAME)
-TRAIN_SOURCES = ["train_host.cpp", "train_tensors.hip", "train_xent.hip"]
+TRAIN_SOURCES = ["train_host.cpp", "train_tensors.hip", "train_xent.hip", "train_rows8.hip",
+                 "train_linear8.hip"]
 ARCH = "gfx950"
 
 

@@ -133,6 +133,112 @@ int check_xent_args(const zero_xent_args* a, bool backward) {
     return ZERO_OK;
 }
 
+// Rows of codes with their scales.
+static int check_codes(const char* name, const void* codes, int64_t stride, const float* scale, int64_t rows,
+                       int64_t dim, int64_t most) {
+    if (rows > 0 && ((dim > 0 && !codes) || !scale)) return fail(ZERO_EINVAL, "%s or its scale is NULL", name);
+    if (stride < ZERO_ROWS8_BYTES(dim) || stride > most)
+        return fail(ZERO_EINVAL, "%s's stride %lld outside [%lld, %lld]", name, (long long)stride,
+                    (long long)ZERO_ROWS8_BYTES(dim), (long long)most);
+    if (off(codes, 16) || stride % 16 != 0)
+        return fail(ZERO_EALIGN, "%s or its stride is not a multiple of 16 bytes", name);
+    if (off(scale, 4)) return fail(ZERO_EALIGN, "%s's scale is not 4-byte aligned", name);
+    return ZERO_OK;
+}
+
+// Rows of a 16- or 32-bit type.
+static int check_rows(const char* name, const void* x, int64_t stride, int64_t rows, int64_t dim, unsigned align) {
+    if (rows > 0 && dim > 0 && !x) return fail(ZERO_EINVAL, "%s is NULL", name);
+    if (stride < dim || stride > int64_t(1) << 31)
+        return fail(ZERO_EINVAL, "%s's stride %lld outside [%lld, 2^31]", name, (long long)stride, (long long)dim);
+    if (off(x, align)) return fail(ZERO_EALIGN, "%s is not %u-byte aligned", name, align);
+    return ZERO_OK;
+}
+
+constexpr int64_t kMostStride = int64_t(1) << 31;
+
+int check_rows8(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, int64_t dim, const void* codes,
+                int64_t codes_stride, const float* scale) {
+    if (dtype != ZERO_FP16 && dtype != ZERO_BF16 && dtype != ZERO_FP32)
+        return fail(ZERO_EINVAL, "dtype %d is not ZERO_FP16, ZERO_BF16 or ZERO_FP32", dtype);
+    if (rows < 0 || rows > INT32_MAX) return fail(ZERO_EINVAL, "rows %lld outside [0, 2^31)", (long long)rows);
+    if (dim < 0 || dim > ZERO_ROWS8_MAX_DIM)
+        return fail(ZERO_EINVAL, "dim %lld outside [0, %d]", (long long)dim, ZERO_ROWS8_MAX_DIM);
+    int rc;
+    if ((rc = check_rows("x", x, x_stride, rows, dim, dtype == ZERO_FP32 ? 4 : 2))) return rc;
+    return check_codes("codes", codes, codes_stride, scale, rows, dim, kMostStride);
+}
+
+int check_glu8_args(const zero_glu8_args* a, bool backward) {
+    if (!a) return fail(ZERO_EINVAL, "args is NULL");
+    if (a->tokens < 0 || a->tokens > INT32_MAX)
+        return fail(ZERO_EINVAL, "tokens %lld outside [0, 2^31)", (long long)a->tokens);
+    if (a->width < 0 || a->width > ZERO_ROWS8_MAX_DIM)
+        return fail(ZERO_EINVAL, "width %lld outside [0, %d]", (long long)a->width, ZERO_ROWS8_MAX_DIM);
+    if (a->dtype != ZERO_FP16 && a->dtype != ZERO_BF16)
+        return fail(ZERO_EINVAL, "dtype %d is not ZERO_FP16 or ZERO_BF16", a->dtype);
+    if (a->kind != ZERO_GLU_SILU && a->kind != ZERO_GLU_GELU)
+        return fail(ZERO_EINVAL, "kind %d is not ZERO_GLU_SILU or ZERO_GLU_GELU", a->kind);
+    const int64_t t = a->tokens, w = a->width;
+    int rc;
+    // the checkpoint, where there is one: with up, both of its parts
+    const bool held = backward || a->gate8 || a->up8;
+    const bool gated = backward ? a->up8 || a->dup : a->up != nullptr;
+    if (held) {
+        if ((rc = check_codes("gate8", a->gate8, a->gate8_stride, a->gate_scale, t, w, kMostStride))) return rc;
+        if (gated) {
+            if ((rc = check_codes("up8", a->up8, a->up8_stride, a->up_scale, t, w, kMostStride))) return rc;
+        } else if (a->up8) {
+            return fail(ZERO_EINVAL, "up8 without up");
+        }
+    }
+    if (backward) {
+        if ((rc = check_rows("dh", a->dh, a->dh_stride, t, w, 2))) return rc;
+        if ((rc = check_rows("dgate", a->dgate, a->dgate_stride, t, w, 2))) return rc;
+        if (gated && (rc = check_rows("dup", a->dup, a->dup_stride, t, w, 2))) return rc;
+        return ZERO_OK;
+    }
+    if ((rc = check_rows("gate", a->gate, a->gate_stride, t, w, 2))) return rc;
+    if (gated && (rc = check_rows("up", a->up, a->up_stride, t, w, 2))) return rc;
+    if (t > 0 && w > 0 && !a->h && !a->h8) return fail(ZERO_EINVAL, "h and h8 are both NULL");
+    if (a->h && (rc = check_rows("h", a->h, a->h_stride, t, w, 2))) return rc;
+    if (a->h8 && (rc = check_codes("h8", a->h8, a->h8_stride, a->h_scale, t, w, kMostStride))) return rc;
+    return ZERO_OK;
+}
+
+int check_linear8_args(const zero_linear8_args* a, bool backward) {
+    if (!a) return fail(ZERO_EINVAL, "args is NULL");
+    if (a->tokens < 0 || a->dim < 0 || a->out < 0) return fail(ZERO_EINVAL, "a size is negative");
+    const size_t need = zero_linear8_workspace_bytes(a->tokens, a->dim, a->out);
+    if (!need)
+        return fail(ZERO_EINVAL, "tokens %lld, dim %lld, out %lld are out of range", (long long)a->tokens,
+                    (long long)a->dim, (long long)a->out);
+    if (a->dtype != ZERO_FP16 && a->dtype != ZERO_BF16)
+        return fail(ZERO_EINVAL, "dtype %d is not ZERO_FP16 or ZERO_BF16", a->dtype);
+    if (a->reserved != 0) return fail(ZERO_EINVAL, "reserved must be 0");
+    const int64_t t = a->tokens, k = a->dim, n = a->out;
+    constexpr int64_t kMost = int64_t(1) << 22;            // the products' descriptors
+    int rc;
+    if ((!backward || a->dw) && (rc = check_codes("x8", a->x8, a->x8_stride, a->x_scale, t, k, kMost))) return rc;
+    if ((!backward || a->dx) && (rc = check_codes("w8", a->w8, a->w8_stride, a->w_scale, n, k, kMost))) return rc;
+    if (backward) {
+        if (!a->dx && !a->dw && !a->db && k > 0 && (t > 0 || n > 0))
+            return fail(ZERO_EINVAL, "dx, dw and db are all NULL");
+        if ((rc = check_rows("dy", a->dy, a->dy_stride, t, n, 2))) return rc;
+        if (a->dx && (rc = check_rows("dx", a->dx, a->dx_stride, t, k, 2))) return rc;
+        if (a->dw && (rc = check_rows("dw", a->dw, a->dw_stride, n, k, 2))) return rc;
+        if (off(a->db, 2)) return fail(ZERO_EALIGN, "db is not 2-byte aligned");
+    } else {
+        if ((rc = check_rows("y", a->y, a->y_stride, t, n, 2))) return rc;
+        if (off(a->bias, 2)) return fail(ZERO_EALIGN, "bias is not 2-byte aligned");
+    }
+    if (!a->workspace) return fail(ZERO_EINVAL, "workspace is NULL");
+    if (off(a->workspace, 256)) return fail(ZERO_EALIGN, "workspace is not 256-byte aligned");
+    if (a->workspace_bytes < need)
+        return fail(ZERO_ESIZE, "workspace_bytes %zu < %zu needed", a->workspace_bytes, need);
+    return ZERO_OK;
+}
+
 }  // namespace zero
 
 using namespace zero;

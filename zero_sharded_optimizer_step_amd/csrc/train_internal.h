@@ -41,4 +41,10 @@ int tensors_constants(const zero_tensors_args* a, bool peers, bool buffers, zero
 
 int check_xent_args(const zero_xent_args* a, bool backward);
 
+// x is what is encoded, or what codes are decoded into.
+int check_rows8(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, int64_t dim, const void* codes,
+                int64_t codes_stride, const float* scale);
+int check_glu8_args(const zero_glu8_args* a, bool backward);
+int check_linear8_args(const zero_linear8_args* a, bool backward);
+
 }  // namespace zero

@@ -38,8 +38,17 @@ enum Epilogue {
     kLse,       // partial maxima and sums of exponentials, target logits
     kProb,      // P, 16 bits
     kSlab,      // fp32 partial products of one slice of k
-    kGrad       // the product times a factor, 16 bits
+    kGrad,      // the product times a factor, 16 bits
+    kPart,      // as kSlab, written over; of all n and k
+    kPlain,     // the product, 16 bits
+    // of 8-bit codes: whole sums times both rows' scales, and a bias
+    kScaledFp16,
+    kScaledBf16
 };
+
+// Beside ZERO_FP16 and ZERO_BF16: two 8-bit codes in an element of 16 bits, so
+// a step is 128 of k and everything else as it is.  Operands are kRows.
+constexpr int kCodes = 100;
 
 // C[n][m] = sum_k A(m, k) B(n, k): m is the contiguous axis of the result.
 struct Product {
@@ -64,7 +73,11 @@ struct Product {
     const zero_xent_result_t* result;   // kGrad: inv_count
     float scale;              // kProb: applied before rounding; kGrad: undone, times grad_scale
     int32_t vocab;
-    const int32_t* kept;      // the backward: how many tokens there are; n or k is their most
+    const int32_t* kept;      // kProb, kSlab, kGrad: how many tokens there are; n or k is their most
+    // kScaled
+    const float* scale_m;
+    const float* scale_n;
+    const unsigned short* bias;   // of m, 16 bits, or NULL
 };
 
 // f(0), f(1) .. f(N - 1), each number a constant.
@@ -87,6 +100,7 @@ __device__ __forceinline__ int swap_cols(int k) { return ((k & 3) | ((k >> 1) & 
 template <int DT>
 __device__ __forceinline__ void mfma(f32x4& c, const s16x8 a, const s16x8 b) {
     if constexpr (DT == ZERO_BF16) asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+    else if constexpr (DT == kCodes) asm volatile("v_mfma_i32_16x16x64_i8 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
     else asm volatile("v_mfma_f32_16x16x32_f16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
 }
 
@@ -266,7 +280,11 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
 
     // The grid is what the chip holds at once; a block walks the tiles of all
     // slices.
-    constexpr bool kTokensAreK = LB == kCols, kTokensAreN = E == kProb || (E == kSlab && !kTokensAreK);
+    constexpr bool kTokensAreK = LB == kCols && (E == kSlab || E == kGrad);
+    constexpr bool kTokensAreN = E == kProb || (E == kSlab && !kTokensAreK);
+    constexpr bool kScaled = E == kScaledFp16 || E == kScaledBf16;
+    constexpr int OT = E == kScaledFp16 ? ZERO_FP16 : (E == kScaledBf16 ? ZERO_BF16 : DT);   // of a 16-bit result
+    static_assert(kScaled == (DT == kCodes), "codes have whole sums");
     const int size_n = kTokensAreN ? *q.kept : q.n, size_k = kTokensAreK ? *q.kept : q.k;
     const int tiles_n = (size_n + BN - 1) / BN;
     const int tiles = q.tiles_m * tiles_n, total = tiles * q.slices;
@@ -501,7 +519,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 }
             };
             split(column);
-        } else if constexpr (E == kSlab) {
+        } else if constexpr (E == kSlab || E == kPart) {
             float* c = reinterpret_cast<float*>(q.c) + static_cast<int64_t>(slice) * q.slab;
             columns([&](auto index) __attribute__((always_inline)) -> void {
                 constexpr int j = decltype(index)::value;
@@ -512,7 +530,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 for (int i = 0; i < FM; ++i) {
                     y[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                     // q.m and ldc are whole quads
-                    if (q.add && n < size_n && i * 16 < end) y[i] = row[i * 4];
+                    if (E == kSlab && q.add && n < size_n && i * 16 < end) y[i] = row[i * 4];
                 }
                 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
@@ -523,15 +541,45 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 }
             });
         } else {
-            const float f = q.scale * q.result->inv_count;
+            float f = 1.0f;
+            if constexpr (E == kGrad) f = q.scale * q.result->inv_count;
             typedef u32x4 eight __attribute__((aligned(2)));
+            // of the lane's m; past the last m the descriptors give 0
+            [[maybe_unused]] f32x4 by[FM], plus[FM];
+            if constexpr (kScaled) {
+                const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                    const_cast<float*>(q.scale_m), 0, q.m * 4, 0x00020000);
+                const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+                    const_cast<unsigned short*>(q.bias), 0, q.m * 2, 0x00020000);
+                #pragma unroll
+                for (int i = 0; i < FM; ++i) {
+                    const int m = m0 + wm + i * 16 + ml;
+                    by[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, m * 4, 0, 0));
+                    plus[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    if (q.bias) {
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            plus[i][e] = lo_to_f32<OT>(__builtin_amdgcn_raw_buffer_load_b16(rb, (m + e) * 2, 0, 0));
+                    }
+                }
+            }
             columns([&](auto index) __attribute__((always_inline)) -> void {
                 constexpr int j = decltype(index)::value;
                 const int n = n0 + wn + j * 16 + nl;
                 unsigned short* row = reinterpret_cast<unsigned short*>(q.c) + n * q.ldc;
+                // an accumulator as it is written; a whole sum is rounded to fp32 first
+                auto result = [&](int i) __attribute__((always_inline)) -> f32x4 {
+                    f32x4 x = taken(acc[i][j]);
+                    if constexpr (kScaled) {
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            x[e] = __builtin_fmaf(static_cast<float>(__float_as_int(x[e])) * lse[j], by[i][e], plus[i][e]);
+                    }
+                    return x;
+                };
                 #pragma unroll
                 for (int i = 0; i < FM; i += 2) {
-                    const u32x4 o = pair<DT>(taken(acc[i][j]), taken(acc[i + 1][j]), f);
+                    const u32x4 o = pair<OT>(result(i), result(i + 1), f);
                     const int m = m0 + wm + i * 16 + pair_m;
                     if (n >= size_n || m >= q.valid_m) continue;
                     if (m + 8 <= q.valid_m) {
@@ -564,12 +612,13 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
         // what the epilogue needs of each token is here long before it
         [[maybe_unused]] int64_t target[FN];
         [[maybe_unused]] float lse[FN];
-        if constexpr (E == kLse || E == kProb) {
+        if constexpr (E == kLse || E == kProb || kScaled) {
             #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 const int n = w.n0 + wn + j * 16 + nl;
-                target[j] = q.target[n < size_n ? n : size_n - 1];
+                if constexpr (!kScaled) target[j] = q.target[n < size_n ? n : size_n - 1];
                 if constexpr (E == kProb) lse[j] = q.lse[n < size_n ? n : size_n - 1];
+                if constexpr (kScaled) lse[j] = q.scale_n[n < size_n ? n : size_n - 1];   // the row's scale
             }
         }
         #pragma unroll
@@ -629,17 +678,6 @@ __global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__
                 if (d + e < dim) o[e] = pack1<DT>(x[e] * f);
         }
     }
-}
-
-// Elements [d, d + 8) of a row of any alignment, zeros past dim.
-__device__ __forceinline__ u32x4 row_piece(const unsigned short* __restrict__ s, int64_t d, int64_t dim) {
-    typedef u32x4 piece __attribute__((aligned(2)));
-    if (d + 8 <= dim) return *reinterpret_cast<const piece*>(s + d);
-    unsigned w[4] = {0u, 0u, 0u, 0u};
-    #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (d + e < dim) w[e / 2] |= static_cast<unsigned>(s[d + e]) << (16 * (e % 2));
-    return u32x4{w[0], w[1], w[2], w[3]};
 }
 
 // Rows of any stride and alignment into rows of ld elements (a multiple of

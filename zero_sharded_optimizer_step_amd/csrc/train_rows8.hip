@@ -1,0 +1,605 @@
+// train_rows8.hip -- rows of 8-bit codes and the gated activation that keeps
+// its input in them (include/zero/train.h).
+//
+// All of it streams: what bounds a large call is HBM.  A row's scale needs
+// its largest magnitude, so the encoders hold a row in registers between the
+// maximum and the codes (a row longer than 16384 is read twice, the second
+// time from the caches); the readers need no row at a time.
+#include <hip/hip_runtime.h>
+
+#include "train_internal.h"
+#include "zero_device.h"
+
+namespace zero {
+namespace {
+
+typedef unsigned short u16x8 __attribute__((ext_vector_type(8)));
+
+// Eight elements of a row: what a lane loads, and the 8 bytes of its codes.
+constexpr int kPiece = 8;
+
+// ------------------------------------------------------------------- scales
+// A row's largest magnitude is taken on the bits: they order as the values
+// do, and an infinity or a NaN is above every number.
+template <int DT>
+constexpr uint32_t kInfinity = DT == ZERO_FP16 ? 0x7C00u : (DT == ZERO_BF16 ? 0x7F80u : 0x7F800000u);
+
+struct Scale {
+    float s, inv;             // 2^e and 2^-e; s is NaN where the row is not finite
+    bool bad;
+};
+
+template <int DT>
+__device__ __forceinline__ Scale scale_of(uint32_t top) {
+    constexpr int kLow = DT == ZERO_FP16 ? -24 : -126, kHigh = DT == ZERO_FP16 ? 9 : 121;
+    uint32_t bits = top;
+    if constexpr (DT != ZERO_FP32) bits = __float_as_uint(lo_to_f32<DT>(top));
+    // the exponent of the top less 6, one more from 127.5 / 64 on
+    int e = static_cast<int>((bits + 0x10000u) >> 23) - 127 - 6;
+    e = e < kLow ? kLow : (e > kHigh ? kHigh : e);
+    Scale r;
+    r.bad = top >= kInfinity<DT>;
+    r.s = r.bad ? __builtin_nanf("") : __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+    r.inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    return r;
+}
+
+// Four codes.  1.5 * 2^23 added to a number of [-127, 127] rounds it to
+// nearest even and leaves it, in two's complement, in the low byte.
+__device__ __forceinline__ unsigned code4(const float x[4], const Scale& k) {
+    unsigned b[4];
+    #pragma unroll
+    for (int e = 0; e < 4; ++e)
+        b[e] = __float_as_uint(__builtin_amdgcn_fmed3f(x[e] * k.inv, -127.0f, 127.0f) + 12582912.0f);
+    const unsigned lo = __builtin_amdgcn_perm(b[1], b[0], 0x0c0c0400u);
+    const unsigned hi = __builtin_amdgcn_perm(b[3], b[2], 0x0c0c0400u);
+    return k.bad ? 0u : lo | hi << 16;
+}
+
+__device__ __forceinline__ void value4(unsigned codes, float s, float o[4]) {
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = static_cast<float>(static_cast<int8_t>(codes >> (8 * e))) * s;
+}
+
+// -------------------------------------------------------------------- pieces
+template <int DT>
+struct Piece {
+    u32x4 w;
+    __device__ __forceinline__ void load(const void* row, int64_t d, int64_t dim) {
+        w = row_piece(static_cast<const unsigned short*>(row), d, dim);
+    }
+    __device__ __forceinline__ void values(float o[8]) const {
+        decode4<DT>(u32x2{w.x, w.y}, o);
+        decode4<DT>(u32x2{w.z, w.w}, o + 4);
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        const u16x8 h = __builtin_bit_cast(u16x8, w & u32x4{0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu});
+        uint32_t t = 0;
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) t = h[e] > t ? h[e] : t;
+        return t;
+    }
+    __device__ __forceinline__ void round(const float o[8]) {
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = pack2<DT>(o[2 * e], o[2 * e + 1]);
+    }
+    // elements [d, d + 8) of a row of any alignment, up to dim
+    __device__ __forceinline__ void store(void* row, int64_t d, int64_t dim) const {
+        typedef u32x4 piece __attribute__((aligned(2)));
+        unsigned short* o = static_cast<unsigned short*>(row) + d;
+        if (d + kPiece <= dim) {
+            *reinterpret_cast<piece*>(o) = w;
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (d + e < dim) o[e] = static_cast<unsigned short>(w[e / 2] >> (16 * (e % 2)));
+        }
+    }
+};
+
+template <>
+struct Piece<ZERO_FP32> {
+    f32x4 w[2];
+    __device__ __forceinline__ void load(const void* row, int64_t d, int64_t dim) {
+        typedef f32x4 quad __attribute__((aligned(4)));
+        const float* s = static_cast<const float*>(row) + d;
+        if (d + kPiece <= dim) {
+            w[0] = *reinterpret_cast<const quad*>(s);
+            w[1] = *reinterpret_cast<const quad*>(s + 4);
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) w[e / 4][e % 4] = d + e < dim ? s[e] : 0.0f;
+        }
+    }
+    __device__ __forceinline__ void values(float o[8]) const {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = w[e / 4][e % 4];
+    }
+    __device__ __forceinline__ uint32_t top() const {
+        uint32_t t = 0;
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const uint32_t b = __float_as_uint(w[e / 4][e % 4]) & 0x7FFFFFFFu;
+            t = b > t ? b : t;
+        }
+        return t;
+    }
+    __device__ __forceinline__ void round(const float o[8]) {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) w[e / 4][e % 4] = o[e];
+    }
+    __device__ __forceinline__ void store(void* row, int64_t d, int64_t dim) const {
+        typedef f32x4 quad __attribute__((aligned(4)));
+        float* o = static_cast<float*>(row) + d;
+        if (d + kPiece <= dim) {
+            *reinterpret_cast<quad*>(o) = w[0];
+            *reinterpret_cast<quad*>(o + 4) = w[1];
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (d + e < dim) o[e] = w[e / 4][e % 4];
+        }
+    }
+};
+
+// Codes are whole pieces up to a multiple of 16 past dim, zeros there.
+template <int DT>
+__device__ __forceinline__ void store_codes(const Piece<DT>& p, const Scale& k, char* row, int64_t d) {
+    float x[8];
+    p.values(x);
+    *reinterpret_cast<u32x2*>(row + d) = u32x2{code4(x, k), code4(x + 4, k)};
+}
+
+// The largest of N values over the TR threads of a row.  Two buffers in turn
+// (`turn`), so one barrier serves a row: a wave that writes one of them again
+// has passed the barrier of the row between, as every reader had before it.
+template <int TR, int N>
+__device__ __forceinline__ void row_max(uint32_t (&t)[N], int turn) {
+    #pragma unroll
+    for (int off = (TR < 64 ? TR : 64) / 2; off > 0; off >>= 1)
+        #pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t u = __shfl_xor(t[i], off, 64);
+            t[i] = u > t[i] ? u : t[i];
+        }
+    if constexpr (TR > 64) {
+        constexpr int kWaves = TR / 64;
+        __shared__ uint32_t s_top[2][N][kWaves];
+        if ((threadIdx.x & 63) == 0)
+            #pragma unroll
+            for (int i = 0; i < N; ++i) s_top[turn][i][threadIdx.x / 64] = t[i];
+        __syncthreads();
+        #pragma unroll
+        for (int i = 0; i < N; ++i)
+            #pragma unroll
+            for (int w = 0; w < kWaves; ++w) t[i] = s_top[turn][i][w] > t[i] ? s_top[turn][i][w] : t[i];
+    }
+}
+
+// How the threads of a block share rows: TR threads a row, P pieces each.
+template <int TR>
+constexpr int kThreads = TR < 256 ? 256 : TR;
+template <int TR>
+constexpr int kRowsABlock = kThreads<TR> / TR;
+
+// ------------------------------------------------------------------- encode
+struct Encode {
+    const char* x;
+    int64_t x_row;            // bytes
+    int64_t rows, dim;
+    char* codes;
+    int64_t codes_row;
+    float* scale;
+};
+
+template <int DT, int TR, int P, bool kHeld>
+__global__ __launch_bounds__(kThreads<TR>) void rows8_encode_kernel(const Encode q) {
+    const int t = threadIdx.x % TR;
+    const int64_t end = (q.dim + 15) / 16 * 16;
+    int turn = 0;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowsABlock<TR> + threadIdx.x / TR; r < q.rows;
+         r += static_cast<int64_t>(gridDim.x) * kRowsABlock<TR>, turn ^= 1) {
+        const char* x = q.x + r * q.x_row;
+        char* codes = q.codes + r * q.codes_row;
+        Piece<DT> p[P];
+        uint32_t top[1] = {0u};
+        for (int64_t base = 0; base < end; base += TR * P * kPiece) {
+            #pragma unroll
+            for (int i = 0; i < P; ++i) p[i].load(x, base + (i * TR + t) * kPiece, q.dim);
+            #pragma unroll
+            for (int i = 0; i < P; ++i) top[0] = p[i].top() > top[0] ? p[i].top() : top[0];
+            if (kHeld) break;
+        }
+        row_max<TR>(top, turn);
+        const Scale k = scale_of<DT>(top[0]);
+        if (t == 0) q.scale[r] = k.s;
+        for (int64_t base = 0; base < end; base += TR * P * kPiece) {
+            #pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int64_t d = base + (i * TR + t) * kPiece;
+                if (!kHeld) p[i].load(x, d, q.dim);
+                if (d < end) store_codes(p[i], k, codes, d);
+            }
+            if (kHeld) break;
+        }
+    }
+}
+
+// ------------------------------------------------------------------- decode
+struct Decode {
+    const char* codes;
+    int64_t codes_row;
+    const float* scale;
+    int64_t rows, dim;
+    char* y;
+    int64_t y_row;            // bytes
+};
+
+template <int DT, int TR, int P>
+__global__ __launch_bounds__(256) void rows8_decode_kernel(const Decode q) {
+    const int t = threadIdx.x % TR;
+    const int64_t first = static_cast<int64_t>(blockIdx.y) * (TR * P * kPiece);
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowsABlock<TR> + threadIdx.x / TR; r < q.rows;
+         r += static_cast<int64_t>(gridDim.x) * kRowsABlock<TR>) {
+        const float s = q.scale[r];
+        const char* codes = q.codes + r * q.codes_row;
+        char* y = q.y + r * q.y_row;
+        u32x2 c[P];
+        #pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int64_t d = first + (i * TR + t) * kPiece;
+            c[i] = d < q.dim ? *reinterpret_cast<const u32x2*>(codes + d) : u32x2{0u, 0u};
+        }
+        #pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int64_t d = first + (i * TR + t) * kPiece;
+            float o[8];
+            value4(c[i].x, s, o);
+            value4(c[i].y, s, o + 4);
+            Piece<DT> p;
+            p.round(o);
+            if (d < q.dim) p.store(y, d, q.dim);
+        }
+    }
+}
+
+// --------------------------------------------------------- gated activation
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kGelu = 1.59576912160573071176f;      // 2 sqrt(2 / pi)
+constexpr float kCubic = 0.044715f;
+
+// act(x) = x p.  exp2 and rcp are the instructions' (1 ulp each), far inside
+// the half step of 16 bits that follows; p below 2^-126 is 0.  Beyond 16
+// gelu's p is 0 or 1 in fp32, so its argument stops there: no power of a
+// large x overflows.
+template <int KIND>
+__device__ __forceinline__ float gate_p(float x) {
+    float z = x;
+    if constexpr (KIND == ZERO_GLU_GELU) {
+        const float c = __builtin_amdgcn_fmed3f(x, -16.0f, 16.0f);
+        z = kGelu * c * __builtin_fmaf(kCubic * c, c, 1.0f);
+    }
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * z));
+}
+// act'(x), with p = gate_p(x); a NaN x gives NaN
+template <int KIND>
+__device__ __forceinline__ float slope(float x, float p) {
+    if constexpr (KIND == ZERO_GLU_SILU) {
+        return p * __builtin_fmaf(x, 1.0f - p, 1.0f);
+    } else {
+        const float c = __builtin_amdgcn_fmed3f(x, -16.0f, 16.0f);
+        return __builtin_fmaf(x * p * (1.0f - p), kGelu * __builtin_fmaf(3.0f * kCubic * c, c, 1.0f), p);
+    }
+}
+
+struct Glu {
+    int64_t tokens, width;
+    // bytes from row to row
+    int64_t gate_row, up_row, h_row, dh_row, dgate_row, dup_row, gate8_row, up8_row, h8_row;
+    const char *gate, *up;
+    char *gate8, *up8, *h, *h8;
+    float *gate_scale, *up_scale, *h_scale;
+    const char* dh;
+    char *dgate, *dup;
+};
+
+template <int DT, int KIND, bool kGated, int TR, int P, bool kHeld>
+__global__ __launch_bounds__(kThreads<TR>) void glu8_forward_kernel(const Glu q) {
+    const int t = threadIdx.x % TR;
+    const int64_t end = (q.width + 15) / 16 * 16;
+    int turn = 0;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowsABlock<TR> + threadIdx.x / TR; r < q.tokens;
+         r += static_cast<int64_t>(gridDim.x) * kRowsABlock<TR>, turn ^= 1) {
+        const char *gate = q.gate + r * q.gate_row, *up = kGated ? q.up + r * q.up_row : nullptr;
+        Piece<DT> g[P], u[kGated ? P : 1], h[P];
+        auto load = [&](int i, int64_t d) __attribute__((always_inline)) -> void {
+            g[i].load(gate, d, q.width);
+            if constexpr (kGated) u[i].load(up, d, q.width);
+        };
+        auto act = [&](int i) __attribute__((always_inline)) -> void {
+            float x[8], o[8];
+            g[i].values(x);
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) o[e] = x[e] * gate_p<KIND>(x[e]);
+            if constexpr (kGated) {
+                u[i].values(x);
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] *= x[e];
+            }
+            h[i].round(o);
+        };
+        uint32_t top[kGated ? 3 : 2] = {};
+        for (int64_t base = 0; base < end; base += TR * P * kPiece) {
+            #pragma unroll
+            for (int i = 0; i < P; ++i) load(i, base + (i * TR + t) * kPiece);
+            #pragma unroll
+            for (int i = 0; i < P; ++i) {
+                act(i);
+                top[0] = g[i].top() > top[0] ? g[i].top() : top[0];
+                top[1] = h[i].top() > top[1] ? h[i].top() : top[1];
+                if constexpr (kGated) top[2] = u[i].top() > top[2] ? u[i].top() : top[2];
+            }
+            if (kHeld) break;
+        }
+        if (q.gate8 || q.h8) row_max<TR>(top, turn);
+        const Scale kg = scale_of<DT>(top[0]), kh = scale_of<DT>(top[1]);
+        Scale ku = kg;
+        if constexpr (kGated) ku = scale_of<DT>(top[2]);
+        if (t == 0) {
+            if (q.gate8) q.gate_scale[r] = kg.s;
+            if (q.h8) q.h_scale[r] = kh.s;
+            if (kGated && q.gate8) q.up_scale[r] = ku.s;
+        }
+        for (int64_t base = 0; base < end; base += TR * P * kPiece) {
+            #pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const int64_t d = base + (i * TR + t) * kPiece;
+                if (!kHeld) {
+                    load(i, d);
+                    act(i);
+                }
+                if (d >= end) continue;
+                if (q.gate8) {
+                    store_codes(g[i], kg, q.gate8 + r * q.gate8_row, d);
+                    if constexpr (kGated) store_codes(u[i], ku, q.up8 + r * q.up8_row, d);
+                }
+                if (q.h8) store_codes(h[i], kh, q.h8 + r * q.h8_row, d);
+                if (q.h) h[i].store(q.h + r * q.h_row, d, q.width);
+            }
+            if (kHeld) break;
+        }
+    }
+}
+
+// dgate or dup may be dh's own memory: a thread has read its piece before it
+// writes there.
+template <int DT, int KIND, bool kGated, int TR, int P>
+__global__ __launch_bounds__(256) void glu8_backward_kernel(const Glu q) {
+    const int t = threadIdx.x % TR;
+    const int64_t first = static_cast<int64_t>(blockIdx.y) * (TR * P * kPiece);
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRowsABlock<TR> + threadIdx.x / TR; r < q.tokens;
+         r += static_cast<int64_t>(gridDim.x) * kRowsABlock<TR>) {
+        const float sg = q.gate_scale[r], su = kGated ? q.up_scale[r] : 1.0f;
+        const char *gate8 = q.gate8 + r * q.gate8_row, *up8 = kGated ? q.up8 + r * q.up8_row : nullptr;
+        const char* dh = q.dh + r * q.dh_row;
+        Piece<DT> p[P];
+        u32x2 cg[P], cu[P];
+        #pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int64_t d = first + (i * TR + t) * kPiece;
+            p[i].load(dh, d, q.width);
+            cg[i] = d < q.width ? *reinterpret_cast<const u32x2*>(gate8 + d) : u32x2{0u, 0u};
+            if constexpr (kGated) cu[i] = d < q.width ? *reinterpret_cast<const u32x2*>(up8 + d) : u32x2{0u, 0u};
+        }
+        #pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int64_t d = first + (i * TR + t) * kPiece;
+            float g[8], u[8], x[8], dg[8], du[8];
+            p[i].values(x);
+            value4(cg[i].x, sg, g);
+            value4(cg[i].y, sg, g + 4);
+            if constexpr (kGated) {
+                value4(cu[i].x, su, u);
+                value4(cu[i].y, su, u + 4);
+            }
+            #pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float pe = gate_p<KIND>(g[e]);
+                dg[e] = x[e] * slope<KIND>(g[e], pe);
+                if constexpr (kGated) {
+                    dg[e] *= u[e];
+                    du[e] = x[e] * (g[e] * pe);
+                }
+            }
+            if (d >= q.width) continue;
+            Piece<DT> o;
+            o.round(dg);
+            o.store(q.dgate + r * q.dgate_row, d, q.width);
+            if constexpr (kGated) {
+                o.round(du);
+                o.store(q.dup + r * q.dup_row, d, q.width);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ launches
+int launched(const char* what) {
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return fail(ZERO_EDEVICE, "%s: %s", what, hipGetErrorString(e));
+    return ZERO_OK;
+}
+
+constexpr int64_t kMostBlocks = 1 << 20;      // times 1024 threads fit the grid's 32 bits
+
+template <int TR>
+unsigned row_blocks(int64_t rows) {
+    const int64_t b = (rows + kRowsABlock<TR> - 1) / kRowsABlock<TR>;
+    return static_cast<unsigned>(b < kMostBlocks ? b : kMostBlocks);
+}
+
+// The threads and pieces of a row for the encoders, by its length.
+template <typename F>
+void by_row(int64_t dim, const F& f) {
+    using std::integral_constant;
+    const int64_t pieces = (dim + 15) / 16 * 2;
+    if (pieces <= 16) f(integral_constant<int, 8>{}, integral_constant<int, 2>{}, std::true_type{});
+    else if (pieces <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{}, std::true_type{});
+    else if (pieces <= 256) f(integral_constant<int, 64>{}, integral_constant<int, 4>{}, std::true_type{});
+    else if (pieces <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2>{}, std::true_type{});
+    else if (pieces <= 1024) f(integral_constant<int, 256>{}, integral_constant<int, 4>{}, std::true_type{});
+    else if (pieces <= 2048) f(integral_constant<int, 256>{}, integral_constant<int, 8>{}, std::true_type{});
+    else f(integral_constant<int, 1024>{}, integral_constant<int, 4>{}, std::false_type{});
+}
+// And for the readers, whose blocks take part of a row.
+template <typename F>
+void by_piece(int64_t dim, const F& f) {
+    using std::integral_constant;
+    const int64_t pieces = (dim + 15) / 16 * 2;
+    if (pieces <= 8) f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+    else if (pieces <= 64) f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+}
+template <int TR, int P>
+unsigned piece_blocks(int64_t dim) {
+    return static_cast<unsigned>((dim + TR * P * kPiece - 1) / (TR * P * kPiece));
+}
+
+template <int DT>
+void encode(const Encode& q, hipStream_t st) {
+    by_row(q.dim, [&](auto tr, auto p, auto held) {
+        constexpr int TR = decltype(tr)::value, P = decltype(p)::value;
+        hipLaunchKernelGGL((rows8_encode_kernel<DT, TR, P, decltype(held)::value>), dim3(row_blocks<TR>(q.rows)),
+                           dim3(kThreads<TR>), 0, st, q);
+    });
+}
+
+template <int DT>
+void decode(const Decode& q, hipStream_t st) {
+    by_piece(q.dim, [&](auto tr, auto p) {
+        constexpr int TR = decltype(tr)::value, P = decltype(p)::value;
+        hipLaunchKernelGGL((rows8_decode_kernel<DT, TR, P>), dim3(row_blocks<TR>(q.rows), piece_blocks<TR, P>(q.dim)),
+                           dim3(256), 0, st, q);
+    });
+}
+
+template <int DT, int KIND, bool kGated>
+void glu_forward(const Glu& q, hipStream_t st) {
+    by_row(q.width, [&](auto tr, auto p, auto held) {
+        constexpr int TR = decltype(tr)::value, P = decltype(p)::value;
+        hipLaunchKernelGGL((glu8_forward_kernel<DT, KIND, kGated, TR, P, decltype(held)::value>),
+                           dim3(row_blocks<TR>(q.tokens)), dim3(kThreads<TR>), 0, st, q);
+    });
+}
+template <int DT, int KIND, bool kGated>
+void glu_backward(const Glu& q, hipStream_t st) {
+    by_piece(q.width, [&](auto tr, auto p) {
+        constexpr int TR = decltype(tr)::value, P = decltype(p)::value;
+        hipLaunchKernelGGL((glu8_backward_kernel<DT, KIND, kGated, TR, P>),
+                           dim3(row_blocks<TR>(q.tokens), piece_blocks<TR, P>(q.width)), dim3(256), 0, st, q);
+    });
+}
+
+template <typename F>
+void by_kind(const zero_glu8_args* a, bool gated, const F& f) {
+    using std::integral_constant;
+    auto kinds = [&](auto dt) {
+        auto gates = [&](auto kind) {
+            if (gated) f(dt, kind, std::true_type{});
+            else f(dt, kind, std::false_type{});
+        };
+        if (a->kind == ZERO_GLU_SILU) gates(integral_constant<int, ZERO_GLU_SILU>{});
+        else gates(integral_constant<int, ZERO_GLU_GELU>{});
+    };
+    if (a->dtype == ZERO_BF16) kinds(integral_constant<int, ZERO_BF16>{});
+    else kinds(integral_constant<int, ZERO_FP16>{});
+}
+
+Glu glu_of(const zero_glu8_args* a) {
+    Glu q;
+    q.tokens = a->tokens;
+    q.width = a->width;
+    q.gate_row = a->gate_stride * 2;
+    q.up_row = a->up_stride * 2;
+    q.h_row = a->h_stride * 2;
+    q.dh_row = a->dh_stride * 2;
+    q.dgate_row = a->dgate_stride * 2;
+    q.dup_row = a->dup_stride * 2;
+    q.gate8_row = a->gate8_stride;
+    q.up8_row = a->up8_stride;
+    q.h8_row = a->h8_stride;
+    q.gate = static_cast<const char*>(a->gate);
+    q.up = static_cast<const char*>(a->up);
+    q.gate8 = static_cast<char*>(a->gate8);
+    q.up8 = static_cast<char*>(a->up8);
+    q.h = static_cast<char*>(a->h);
+    q.h8 = static_cast<char*>(a->h8);
+    q.gate_scale = a->gate_scale;
+    q.up_scale = a->up_scale;
+    q.h_scale = a->h_scale;
+    q.dh = static_cast<const char*>(a->dh);
+    q.dgate = static_cast<char*>(a->dgate);
+    q.dup = static_cast<char*>(a->dup);
+    return q;
+}
+
+}  // namespace
+}  // namespace zero
+
+using namespace zero;
+
+extern "C" {
+
+int zero_rows8_encode(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, int64_t dim, void* codes,
+                      int64_t codes_stride, float* scale, void* stream) {
+    clear_error();
+    const int rc = check_rows8(x, x_stride, dtype, rows, dim, codes, codes_stride, scale);
+    if (rc || rows == 0) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const Encode q = {static_cast<const char*>(x), x_stride * (dtype == ZERO_FP32 ? 4 : 2), rows, dim,
+                      static_cast<char*>(codes), codes_stride, scale};
+    if (dtype == ZERO_BF16) encode<ZERO_BF16>(q, st);
+    else if (dtype == ZERO_FP16) encode<ZERO_FP16>(q, st);
+    else encode<ZERO_FP32>(q, st);
+    return launched("row encode kernel launch");
+}
+
+int zero_rows8_decode(const void* codes, int64_t codes_stride, const float* scale, int64_t rows, int64_t dim, void* y,
+                      int64_t y_stride, int32_t dtype, void* stream) {
+    clear_error();
+    const int rc = check_rows8(y, y_stride, dtype, rows, dim, codes, codes_stride, scale);
+    if (rc || rows == 0 || dim == 0) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const Decode q = {static_cast<const char*>(codes), codes_stride, scale, rows, dim,
+                      static_cast<char*>(y), y_stride * (dtype == ZERO_FP32 ? 4 : 2)};
+    if (dtype == ZERO_BF16) decode<ZERO_BF16>(q, st);
+    else if (dtype == ZERO_FP16) decode<ZERO_FP16>(q, st);
+    else decode<ZERO_FP32>(q, st);
+    return launched("row decode kernel launch");
+}
+
+int zero_glu8_forward(const zero_glu8_args* a, void* stream) {
+    clear_error();
+    const int rc = check_glu8_args(a, false);
+    if (rc || a->tokens == 0 || a->width == 0) return rc;
+    const Glu q = glu_of(a);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    by_kind(a, a->up != nullptr, [&](auto dt, auto kind, auto gated) {
+        glu_forward<decltype(dt)::value, decltype(kind)::value, decltype(gated)::value>(q, st);
+    });
+    return launched("gated activation kernel launch");
+}
+
+int zero_glu8_backward(const zero_glu8_args* a, void* stream) {
+    clear_error();
+    const int rc = check_glu8_args(a, true);
+    if (rc || a->tokens == 0 || a->width == 0) return rc;
+    const Glu q = glu_of(a);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    by_kind(a, a->up8 != nullptr, [&](auto dt, auto kind, auto gated) {
+        glu_backward<decltype(dt)::value, decltype(kind)::value, decltype(gated)::value>(q, st);
+    });
+    return launched("gated activation gradient kernel launch");
+}
+
+}  // extern "C"

@@ -89,5 +89,16 @@ __device__ __forceinline__ void adamw1(float g, float& p, float& m, float& v, co
     p = p * k.decay - k.step_size * (m / d);
 }
 
+// Elements [d, d + 8) of a row of any alignment, zeros past dim.
+__device__ __forceinline__ u32x4 row_piece(const unsigned short* __restrict__ s, int64_t d, int64_t dim) {
+    typedef u32x4 piece __attribute__((aligned(2)));
+    if (d + 8 <= dim) return *reinterpret_cast<const piece*>(s + d);
+    unsigned w[4] = {0u, 0u, 0u, 0u};
+    #pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (d + e < dim) w[e / 2] |= static_cast<unsigned>(s[d + e]) << (16 * (e % 2));
+    return u32x4{w[0], w[1], w[2], w[3]};
+}
+
 }  // namespace
 }  // namespace zero

@@ -1,6 +1,8 @@
 """Binding of the training operators (include/zero/train.h): AdamW over a
 list of tensors with 32-bit or 8-bit states, the conversion between the two,
-and the softmax cross entropy of a large vocabulary with its gradient.
+the softmax cross entropy of a large vocabulary with its gradient, rows of
+8-bit codes, and the gated activation and the product that read them, each
+with its gradient.
 
 As in the package's other calls, torch tensors become device pointers, the
 current torch stream becomes the hipStream_t, negative status codes become
@@ -15,9 +17,10 @@ from typing import Optional, Sequence
 # imported at the end of the package's own module, which defines these
 from . import _dptr, _need, _stream, _torch, dtype_code
 from ._abi import check, lib, zero_global_t
-from ._train_abi import (ZERO_MAX_GROUPS, ZERO_STATE8_BLOCK, train_lib, zero_adam_group_t,
-                         zero_tensor_t, zero_tensors_args, zero_tensors_plan_t,
-                         zero_tensors_scalars_t, zero_xent_args, zero_xent_result_t)
+from ._train_abi import (ZERO_GLU_GELU, ZERO_GLU_SILU, ZERO_MAX_GROUPS, ZERO_STATE8_BLOCK, train_lib,
+                         zero_adam_group_t, zero_glu8_args, zero_linear8_args, zero_tensor_t,
+                         zero_tensors_args, zero_tensors_plan_t, zero_tensors_scalars_t, zero_xent_args,
+                         zero_xent_result_t)
 
 
 def _on_device(**tensors) -> None:
@@ -376,3 +379,222 @@ def zero_xent_backward(args: XentArgs, stream=None) -> None:
     _launching(args.x)
     check(train_lib().zero_xent_backward(ctypes.byref(a), _stream(stream)),
           "zero_xent_backward")
+
+
+# ----------------------------------------------------------- rows of 8-bit codes
+def rows8_stride(dim: int) -> int:
+    """Bytes that a row of dim codes takes: dim rounded up to a multiple of
+    16, zeros from dim on."""
+    return (dim + 15) // 16 * 16
+
+
+def _rows(name: str, t, rows: int, cols: int, dtype) -> int:
+    """The row stride of a matrix [rows, cols] of any row stride."""
+    if t.dtype != dtype:
+        raise ValueError("%s is %s, expected %s" % (name, t.dtype, dtype))
+    if t.shape != (rows, cols):
+        raise ValueError("%s is %s, expected %s" % (name, tuple(t.shape), (rows, cols)))
+    s = t.stride()
+    if cols > 1 and rows > 0 and s[1] != 1:
+        raise ValueError("%s's rows are not contiguous" % name)
+    # a single row may carry any stride; the library wants cols or more
+    return s[0] if rows > 1 else max(s[0], cols)
+
+
+def _codes(name: str, t, scale, rows: int, dim: int) -> int:
+    """The row stride of codes int8 [rows, rows8_stride(dim) or more]."""
+    torch = _torch()
+    wide = rows8_stride(dim)
+    if scale is None or t is None:
+        raise ValueError("%s and its scale are given together" % name)
+    if t.dtype != torch.int8:
+        raise ValueError("%s is %s, expected torch.int8" % (name, t.dtype))
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < wide:
+        raise ValueError("%s is %s, expected [%d, %d or more]" % (name, tuple(t.shape), rows, wide))
+    s = t.stride()
+    if wide > 0 and rows > 0 and s[1] != 1:
+        raise ValueError("%s's rows are not contiguous" % name)
+    if scale.dtype != torch.float32 or scale.numel() != rows or not scale.is_contiguous():
+        raise ValueError("%s's scale must be %d contiguous float32 values" % (name, rows))
+    # one row, or rows of nothing, may carry any stride, also none that is a multiple of 16
+    return s[0] if rows > 1 and wide > 0 else wide
+
+
+def zero_rows8_encode(x, codes, scale, stream=None) -> None:
+    """Rows of x [rows, dim] (fp32, bf16 or fp16, any row stride) into codes
+    int8 [rows, rows8_stride(dim) or more] and scale fp32 [rows]."""
+    if x.dim() != 2:
+        raise ValueError("x is %s; expected [rows, dim]" % (tuple(x.shape),))
+    rows, dim = x.shape
+    xs, cs = _rows("x", x, rows, dim, x.dtype), _codes("codes", codes, scale, rows, dim)
+    _on_device(x=x, codes=codes, scale=scale)
+    _launching(x)
+    check(train_lib().zero_rows8_encode(x.data_ptr(), xs, dtype_code(x.dtype), rows, dim, codes.data_ptr(), cs,
+                                        scale.data_ptr(), _stream(stream)), "zero_rows8_encode")
+
+
+def zero_rows8_decode(codes, scale, y, stream=None) -> None:
+    """The rows that codes and scale stand for into y [rows, dim] (fp32, bf16
+    or fp16, any row stride)."""
+    if y.dim() != 2:
+        raise ValueError("y is %s; expected [rows, dim]" % (tuple(y.shape),))
+    rows, dim = y.shape
+    ys, cs = _rows("y", y, rows, dim, y.dtype), _codes("codes", codes, scale, rows, dim)
+    _on_device(y=y, codes=codes, scale=scale)
+    _launching(y)
+    check(train_lib().zero_rows8_decode(codes.data_ptr(), cs, scale.data_ptr(), rows, dim, y.data_ptr(), ys,
+                                        dtype_code(y.dtype), _stream(stream)), "zero_rows8_decode")
+
+
+# ------------------------------------------------------------- gated activation
+_GLU_KINDS = {"silu": ZERO_GLU_SILU, "gelu": ZERO_GLU_GELU}
+
+
+@dataclass
+class Glu8Args:
+    """Builds a zero_glu8_args from torch tensors: gate, up, h, dh, dgate and
+    dup [tokens, width] (fp16 or bf16, any row stride), gate8, up8 and h8 int8
+    [tokens, rows8_stride(width) or more] with scales fp32 [tokens].  Without
+    up the activation is not gated (then no up8 and dup either).  The forward
+    takes gate and up and writes h, h8 or both, and, where gate8 is given,
+    the checkpoint gate8 and up8; the backward takes dh and the checkpoint
+    alone."""
+    kind: str = "silu"
+    gate: object = None
+    up: object = None
+    gate8: object = None
+    gate_scale: object = None
+    up8: object = None
+    up_scale: object = None
+    h: object = None
+    h8: object = None
+    h_scale: object = None
+    dh: object = None
+    dgate: object = None
+    dup: object = None
+
+    def c_args(self, backward: bool) -> zero_glu8_args:
+        a = zero_glu8_args()
+        first = self.dh if backward else self.gate
+        if first is None or first.dim() != 2:
+            raise ValueError("%s must be a tensor [tokens, width]" % ("dh" if backward else "gate"))
+        if self.kind not in _GLU_KINDS:
+            raise ValueError("kind is %r, expected one of %s" % (self.kind, sorted(_GLU_KINDS)))
+        t, w = first.shape
+        a.tokens, a.width = t, w
+        a.dtype, a.kind = dtype_code(first.dtype), _GLU_KINDS[self.kind]
+        given = {}
+        for name in ("dh", "dgate", "dup") if backward else ("gate", "up", "h"):
+            m = getattr(self, name)
+            if m is None:
+                continue
+            given[name] = m
+            setattr(a, name + "_stride", _rows(name, m, t, w, first.dtype))
+            setattr(a, name, m.data_ptr())
+        for name, scale in (("gate8", "gate_scale"), ("up8", "up_scale"), ("h8", "h_scale")):
+            codes, s = getattr(self, name), getattr(self, scale)
+            if codes is None and s is None or backward and name == "h8":
+                continue
+            setattr(a, name + "_stride", _codes(name, codes, s, t, w))
+            given[name], given[scale] = codes, s
+            setattr(a, name, codes.data_ptr())
+            setattr(a, scale, s.data_ptr())
+        for name in (("gate8", "dgate") if backward else ()):
+            if name not in given:
+                raise ValueError("the backward needs %s" % name)
+        _on_device(**given)
+        return a
+
+
+def zero_glu8_forward(args: Glu8Args, stream=None) -> None:
+    """h, h8 and the checkpoint of args, as far as they are given."""
+    a = args.c_args(False)
+    _launching(args.gate)
+    check(train_lib().zero_glu8_forward(ctypes.byref(a), _stream(stream)), "zero_glu8_forward")
+
+
+def zero_glu8_backward(args: Glu8Args, stream=None) -> None:
+    """dgate and dup of args from dh and the checkpoint."""
+    a = args.c_args(True)
+    _launching(args.dh)
+    check(train_lib().zero_glu8_backward(ctypes.byref(a), _stream(stream)), "zero_glu8_backward")
+
+
+# ---------------------------------------------------------------- 8-bit products
+def zero_linear8_workspace_bytes(tokens: int, dim: int, out: int) -> int:
+    return train_lib().zero_linear8_workspace_bytes(tokens, dim, out)
+
+
+@dataclass
+class Linear8Args:
+    """Builds a zero_linear8_args from torch tensors: x8 int8 [tokens,
+    rows8_stride(dim) or more] and w8 int8 [out, the same] with scales fp32
+    [tokens] and [out]; bias [out] or None and y [tokens, out] for the
+    forward; dy [tokens, out] and those of dx [tokens, dim], dw [out, dim]
+    and db [out] that are wanted for the backward (fp16 or bf16, matrices of
+    any row stride).  A backward without dx needs no w8, one without dw no
+    x8."""
+    x8: object
+    x_scale: object
+    w8: object
+    w_scale: object
+    dim: int
+    workspace: object
+    bias: object = None
+    y: object = None
+    dy: object = None
+    dx: object = None
+    dw: object = None
+    db: object = None
+
+    def c_args(self, backward: bool) -> zero_linear8_args:
+        a = zero_linear8_args()
+        first = self.dy if backward else self.y
+        if first is None or first.dim() != 2:
+            raise ValueError("%s must be a tensor [tokens, out]" % ("dy" if backward else "y"))
+        (t, n), k, dtype = first.shape, self.dim, first.dtype
+        a.tokens, a.dim, a.out, a.dtype = t, k, n, dtype_code(dtype)
+        given = {"workspace": self.workspace}
+        for name, shape in ((("dy", (t, n)), ("dx", (t, k)), ("dw", (n, k))) if backward else (("y", (t, n)),)):
+            m = getattr(self, name)
+            if m is None:
+                continue
+            given[name] = m
+            setattr(a, name + "_stride", _rows(name, m, *shape, dtype))
+            setattr(a, name, m.data_ptr())
+        for name, scale, rows, used in (("x8", "x_scale", t, not backward or self.dw is not None),
+                                        ("w8", "w_scale", n, not backward or self.dx is not None)):
+            if not used:
+                continue
+            codes, s = getattr(self, name), getattr(self, scale)
+            setattr(a, name + "_stride", _codes(name, codes, s, rows, k))
+            given[name], given[scale] = codes, s
+            setattr(a, name, codes.data_ptr())
+            setattr(a, scale, s.data_ptr())
+        name = "db" if backward else "bias"
+        v = getattr(self, name)
+        if v is not None:
+            if v.dtype != dtype or v.numel() != n or not v.is_contiguous():
+                raise ValueError("%s must be %d contiguous %s values" % (name, n, dtype))
+            given[name] = v
+            setattr(a, name, v.data_ptr())
+        if not self.workspace.is_contiguous():
+            raise ValueError("workspace is not contiguous")
+        _on_device(**given)
+        a.workspace = self.workspace.data_ptr()
+        a.workspace_bytes = self.workspace.numel() * self.workspace.element_size()
+        return a
+
+
+def zero_linear8_forward(args: Linear8Args, stream=None) -> None:
+    """y of args."""
+    a = args.c_args(False)
+    _launching(args.y)
+    check(train_lib().zero_linear8_forward(ctypes.byref(a), _stream(stream)), "zero_linear8_forward")
+
+
+def zero_linear8_backward(args: Linear8Args, stream=None) -> None:
+    """Those of dx, dw and db of args that are given."""
+    a = args.c_args(True)
+    _launching(args.dy)
+    check(train_lib().zero_linear8_backward(ctypes.byref(a), _stream(stream)), "zero_linear8_backward")
