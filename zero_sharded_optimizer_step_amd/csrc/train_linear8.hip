@@ -26,148 +26,314 @@ struct Few {
     int64_t ldy;              // elements
 };
 
-// Up to 16 NF tokens: w8 is read once and nothing else counts, so the
-// fragments go from memory to registers, many loads at a time.  A block takes
-// 16 rows of w8; its four waves take every fourth 128 of k, and the sums,
-// whole numbers, meet in LDS.
+// Few tokens: w8 is read once and nothing else counts.  A block takes 16 rows
+// of w8 at a time, `groups` times, and 16 NF tokens; its four waves take every
+// fourth 128 of k, each on its own, and their sums, whole numbers, meet in
+// LDS.  The loads of the next rows are under way meanwhile.  They go to LDS
+// with 8 lanes along a row: as fragments straight into registers, a row to a
+// lane, every lane is an address of its own, and the 16 bytes a cycle and CU
+// that this gives bound the kernel (1 token x 4096 x 16384 15.7 us, 64 tokens
+// 46).  Blocks begin at unlike k, or all of them would meet in the same
+// channels of memory.
+constexpr int kFewWaves = 4, kMostGroups = 16;
 template <int OT, int NF>
-__global__ __launch_bounds__(256) void few8_kernel(const Few q) {
-    constexpr int kGroup = 2;                              // of 128 k a wave and turn
-    __shared__ i32x4 s_sum[4][NF][64];
+__global__ __launch_bounds__(kFewWaves * 64) void few8_kernel(const Few q) {
+    constexpr int W = kFewWaves, kRowsBytes = 16 * 128, kSlot = (1 + NF) * kRowsBytes, kLoads = 2 * (1 + NF);
+    __shared__ __attribute__((aligned(1024))) char s0[W][kSlot];
+    __shared__ __attribute__((aligned(1024))) char s1[W][kSlot];
+    __shared__ __attribute__((aligned(1024))) char s2[W][kSlot];
+    __shared__ i32x4 s_sum[2][W][NF][64];
+    __shared__ f32x4 s_scale[kMostGroups][4], s_bias[kMostGroups][4];
     const int lane = threadIdx.x & 63, s = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int m0 = blockIdx.x * 16;
+    const int n0 = blockIdx.y * (16 * NF);
+    const int step_m = gridDim.x * 16;                     // from group to group
+    const int groups = (q.out - static_cast<int>(blockIdx.x) * 16 + step_m - 1) / step_m;
+    // a thread has an output channel of each group
+    {
+        const int i = threadIdx.x / 16, m = blockIdx.x * 16 + i * step_m + threadIdx.x % 16;
+        if (i < groups) {
+            const int at = m < q.out ? m : q.out - 1;
+            s_scale[i][s / 4][s % 4] = q.w_scale[at];
+            s_bias[i][s / 4][s % 4] = q.bias ? lo_to_f32<OT>(q.bias[at]) : 0.0f;
+        }
+    }
+    // a wave finishes 16 tokens
+    const int n = n0 + wave * 16 + s;
+    const bool mine = wave < NF && n < q.tokens;
+    const float sx = mine ? q.x_scale[n] : 0.0f;
+    __syncthreads();
     auto records = [](int64_t bytes) { return static_cast<int>(bytes < 0x7ffffff0 ? bytes : 0x7ffffff0); };
-    const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char*>(q.w + m0 * q.ldw), 0, records((q.out - m0) * q.ldw), 0x00020000);
-    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(q.x), 0,
-                                                                        records(q.tokens * q.ldx), 0x00020000);
-    const uint32_t oa = static_cast<uint32_t>(s * q.ldw), ob = static_cast<uint32_t>(s * q.ldx);
-    const uint32_t next = static_cast<uint32_t>(16 * q.ldx);
-    struct Pieces {
-        u32x4 a[kGroup][2], b[kGroup][2][NF];
-    };
-    // k of this lane's piece p of block `block` of 128: both operands agree on it
-    auto load = [&](Pieces& f, int block) __attribute__((always_inline)) -> void {
+    const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(q.x + n0 * q.ldx), 0, records((q.tokens - n0) * q.ldx), 0x00020000);
+    const int blocks = q.k > 0 ? (q.k + 127) / 128 : 1;    // of 128 of k
+    const int mine_k = (blocks + W - 1) / W;               // steps of a group
+    const int turn = static_cast<int>(static_cast<unsigned>(blockIdx.x / kXcds * W) % static_cast<unsigned>(blocks));
+    // Row r's piece c of 16 bytes lies where piece c ^ swap_rows(r) would: a
+    // load's 8 rows below the first 8 have bit 2 of it the other way.
+    const int row = lane / 8, piece = (lane % 8) ^ swap_rows(row);
+    const uint32_t oa = static_cast<uint32_t>(row * q.ldw), ob = static_cast<uint32_t>(row * q.ldx);
+    // the next step's loads: two of 8 rows for each 16; past the last group all give 0
+    int load_m = blockIdx.x * 16, load_i = wave;
+    auto load = [&](char* slot) __attribute__((always_inline)) -> void {
+        const __amdgpu_buffer_rsrc_t ra = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char*>(q.w + load_m * q.ldw), 0, load_m < q.out ? records((q.out - load_m) * q.ldw) : 0, 0x00020000);
+        const int block = load_i + turn < blocks ? load_i + turn : load_i + turn - blocks;
         #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
+        for (int p = 0; p < 2; ++p) {
+            const int k = block * 128 + (piece ^ (p * 4)) * 16;
+            const bool in = load_i < blocks && k < q.k;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (ZERO_LDS void*)(slot + p * 1024), 16,
+                                                     in ? oa + p * 8 * static_cast<uint32_t>(q.ldw) + k : kNowhere, 0, 0, 0);
             #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int k = (block + 4 * u) * 128 + g * 32 + p * 16;
-                f.a[u][p] = __builtin_amdgcn_raw_buffer_load_b128(ra, k < q.k ? oa + k : kNowhere, 0, 0);
-                #pragma unroll
-                for (int j = 0; j < NF; ++j)
-                    f.b[u][p][j] = __builtin_amdgcn_raw_buffer_load_b128(rb, k < q.k ? ob + j * next + k : kNowhere, 0, 0);
-            }
+            for (int j = 0; j < NF; ++j)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                    rb, (ZERO_LDS void*)(slot + (1 + j) * kRowsBytes + p * 1024), 16,
+                    in ? ob + (j * 16 + p * 8) * static_cast<uint32_t>(q.ldx) + k : kNowhere, 0, 0, 0);
+        }
+        load_i += W;
+        if (load_i >= mine_k * W) {
+            load_i = wave;
+            load_m += step_m;
+        }
     };
     i32x4 acc[NF] = {};
-    auto multiply = [&](const Pieces& f) __attribute__((always_inline)) -> void {
+    const uint32_t at = s * 128 + (g ^ swap_rows(s)) * 16;
+    int group = 0, done = 0;
+    auto finish = [&]() __attribute__((always_inline)) -> void {
+        i32x4 (&sums)[W][NF][64] = s_sum[group & 1];
         #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
+        for (int j = 0; j < NF; ++j) {
+            sums[wave][j][lane] = acc[j];
+            acc[j] = i32x4{0, 0, 0, 0};
+        }
+        // the loads under way stay so: nothing but LDS is waited for
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        __builtin_amdgcn_s_barrier();
+        if (mine) {
+            i32x4 sum = sums[0][wave][lane];
             #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                #pragma unroll
-                for (int j = 0; j < NF; ++j)
-                    acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, f.a[u][p]),
-                                                                   __builtin_bit_cast(i32x4, f.b[u][p][j]), acc[j], 0, 0, 0);
+            for (int w = 1; w < W; ++w) sum += sums[w][wave][lane];
+            const f32x4 sw = s_scale[group][g], b = s_bias[group][g];
+            const int m = blockIdx.x * 16 + group * step_m + g * 4;
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (m + e < q.out)
+                    q.y[n * q.ldy + m + e] = pack1<OT>(__builtin_fmaf(static_cast<float>(sum[e]) * sx, sw[e], b[e]));
+        }
+        ++group;
+        done = 0;
     };
-    const int blocks = (q.k + 127) / 128;
-    Pieces f0, f1;
-    load(f0, wave);
-    for (int b = wave; b < blocks; b += 8 * kGroup) {
-        load(f1, b + 4 * kGroup);
-        multiply(f0);
-        load(f0, b + 8 * kGroup);
-        multiply(f1);
+    auto step = [&](const char* use, char* fill) __attribute__((always_inline)) -> void {
+        load(fill);
+        __builtin_amdgcn_s_waitcnt(0x0f70 | ((2 * kLoads) & 15) | ((2 * kLoads) >> 4) << 14);
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const ZERO_LDS char* from = (const ZERO_LDS char*)use + (at ^ (h * 64));
+            const i32x4 a = *(const ZERO_LDS i32x4*)from;
+            #pragma unroll
+            for (int j = 0; j < NF; ++j)
+                acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, *(const ZERO_LDS i32x4*)(from + (1 + j) * kRowsBytes),
+                                                               acc[j], 0, 0, 0);
+        }
+        // read before it is filled again
+        __builtin_amdgcn_s_waitcnt(0xc07f);
+        if (++done == mine_k) finish();
+    };
+    char *a0 = s0[wave], *a1 = s1[wave], *a2 = s2[wave];
+    load(a0);
+    load(a1);
+    const int steps = groups * mine_k;
+    for (int i = 0; i < steps; i += 3) {
+        step(a0, a2);
+        if (i + 1 < steps) step(a1, a0);
+        if (i + 2 < steps) step(a2, a1);
+    }
+    // no load outlives the block
+    __builtin_amdgcn_s_waitcnt(0x0f70);
+}
+
+// What the gradient's products read, made in one launch, each part a range of
+// blocks: w^ and x^ in 16 bits, dy's rows where they are not whole pieces, and
+// sums of dy's columns over shares of its rows.
+struct Held {
+    const char* codes;        // at the first column
+    int64_t stride;
+    const float* scale;
+    int64_t rows;
+    int32_t wide, pieces;     // columns, and pieces of 8 of them
+    unsigned short* out;
+    int64_t ld;               // elements
+};
+struct Prepare {
+    Held held[2];
+    const unsigned short* dy;
+    int64_t dy_stride, tokens, out;
+    unsigned short* dyr;
+    int64_t dyr_ld;
+    int64_t share;            // rows of one share of the column sums
+    int32_t column_blocks;    // of 256 columns
+    float* part;              // [shares][out], or
+    unsigned short* db;       // the only share's sums in 16 bits
+    uint32_t ends[4];         // the blocks' ranges end here
+};
+
+// A block's pieces, of 256 threads: enough for their loads to be on their way
+// together.
+constexpr int kPrepPieces = 2;
+
+template <int DT>
+__device__ __forceinline__ void write_held(const Held& h, uint32_t block) {
+    // the block's first piece; from there 32 bits do
+    const int64_t first = static_cast<int64_t>(block) * (256 * kPrepPieces);
+    const int64_t row0 = first / h.pieces;
+    const uint32_t in_row = static_cast<uint32_t>(first - row0 * h.pieces);
+    u32x2 c[kPrepPieces];
+    float s[kPrepPieces];
+    int64_t r[kPrepPieces];
+    int d[kPrepPieces];
+    #pragma unroll
+    for (int i = 0; i < kPrepPieces; ++i) {
+        const uint32_t at = in_row + i * 256 + threadIdx.x, down = at / static_cast<uint32_t>(h.pieces);
+        r[i] = row0 + down;
+        d[i] = static_cast<int>(at - down * h.pieces) * 8;
+        if (r[i] >= h.rows) continue;
+        c[i] = *reinterpret_cast<const u32x2*>(h.codes + r[i] * h.stride + d[i]);
+        s[i] = h.scale[r[i]];
     }
     #pragma unroll
-    for (int j = 0; j < NF; ++j) s_sum[wave][j][lane] = acc[j];
-    __syncthreads();
-    // a wave finishes 16 tokens
-    const int n = wave * 16 + s;
-    if (wave >= NF || n >= q.tokens) return;
-    const i32x4 sum = s_sum[0][wave][lane] + s_sum[1][wave][lane] + s_sum[2][wave][lane] + s_sum[3][wave][lane];
-    const float sx = q.x_scale[n];
-    #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int m = m0 + g * 4 + e;
-        if (m >= q.out) break;
-        const float b = q.bias ? lo_to_f32<OT>(q.bias[m]) : 0.0f;
-        q.y[n * q.ldy + m] = pack1<OT>(__builtin_fmaf(static_cast<float>(sum[e]) * sx, q.w_scale[m], b));
+    for (int i = 0; i < kPrepPieces; ++i) {
+        if (r[i] >= h.rows) continue;
+        float x[8];
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = static_cast<float>(static_cast<int8_t>(c[i][e / 4] >> (8 * (e % 4)))) * s[i];
+        *reinterpret_cast<u32x4*>(h.out + r[i] * h.ld + d[i]) =
+            u32x4{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3]), pack2<DT>(x[4], x[5]), pack2<DT>(x[6], x[7])};
     }
 }
 
-// Sums of n columns over rows [first, last) of a block's share; 256 columns a
-// block, eight rows at a time.
-struct ColumnSum {
-    const unsigned short* dy;
-    int64_t ld;               // elements
-    int64_t rows, out, share; // rows of one share
-    float* part;              // [shares][out]
-};
+// 256 columns a block, eight rows at a time.
 template <int DT>
-__global__ __launch_bounds__(256) void column_sum_kernel(const ColumnSum q) {
+__device__ __forceinline__ void column_sums(const Prepare& q, uint32_t block) {
     __shared__ float s_sum[8][256];
     const int col = threadIdx.x & 31, row = threadIdx.x >> 5;
-    const int64_t d = static_cast<int64_t>(blockIdx.x) * 256 + col * 8;
-    const int64_t first = blockIdx.y * q.share, last = first + q.share < q.rows ? first + q.share : q.rows;
+    const uint32_t across = block % q.column_blocks;
+    const int64_t down = block / q.column_blocks;
+    // eight columns a thread; past the last the last eight again
+    int64_t d = static_cast<int64_t>(across) * 256 + col * 8;
+    if (q.out >= 8 && d > q.out - 8) d = q.out - 8;
+    const int64_t first = down * q.share, last = first + q.share < q.tokens ? first + q.share : q.tokens;
     float sum[8] = {};
-    #pragma unroll 4
-    for (int64_t r = first + row; r < last; r += 8) {
-        const u32x4 w = row_piece(q.dy + r * q.ld, d, q.out);
-        float x[8];
-        decode4<DT>(u32x2{w.x, w.y}, x);
-        decode4<DT>(u32x2{w.z, w.w}, x + 4);
-        #pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] += x[e];
-    }
+    // kDeep rows' loads on their way together; past the last row its own again, for nothing
+    constexpr int kDeep = 8;
+    auto add = [&](auto piece) __attribute__((always_inline)) -> void {
+        for (int64_t r = first + row; r < last; r += 8 * kDeep) {
+            u32x4 w[kDeep];
+            #pragma unroll
+            for (int i = 0; i < kDeep; ++i) w[i] = piece(q.dy + (r + 8 * i < last ? r + 8 * i : r) * q.dy_stride);
+            #pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                float x[8];
+                decode4<DT>(u32x2{w[i].x, w[i].y}, x);
+                decode4<DT>(u32x2{w[i].z, w[i].w}, x + 4);
+                #pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += r + 8 * i < last ? x[e] : 0.0f;
+            }
+        }
+    };
+    typedef u32x4 eight __attribute__((aligned(2)));
+    if (q.out >= 8) add([&](const unsigned short* at) { return u32x4(*reinterpret_cast<const eight*>(at + d)); });
+    else add([&](const unsigned short* at) { return row_piece(at, d, q.out); });
+    // columns of two threads have the same sums twice
+    const int64_t place = d - static_cast<int64_t>(across) * 256;
     #pragma unroll
-    for (int e = 0; e < 8; ++e) s_sum[row][col * 8 + e] = sum[e];
+    for (int e = 0; e < 8; ++e)
+        if (place + e >= 0) s_sum[row][place + e] = sum[e];
     __syncthreads();
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t n = static_cast<int64_t>(across) * 256 + threadIdx.x;
     if (n >= q.out) return;
     float total = 0.0f;
     #pragma unroll
     for (int r = 0; r < 8; ++r) total += s_sum[r][threadIdx.x];
-    q.part[blockIdx.y * q.out + n] = total;
-}
-template <int DT>
-__global__ __launch_bounds__(256) void column_join_kernel(const float* __restrict__ part, int shares, int64_t out,
-                                                          unsigned short* __restrict__ db) {
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (n >= out) return;
-    float total = 0.0f;
-    for (int i = 0; i < shares; ++i) total += part[i * out + n];
-    db[n] = pack1<DT>(total);
+    if (q.db) q.db[n] = pack1<DT>(total);
+    else q.part[down * q.out + n] = total;
 }
 
-// The slices' sum in 16 bits; slices in order.
 template <int DT>
-__global__ __launch_bounds__(256) void slice_sum_kernel(const float* __restrict__ slabs, int n_slabs, int64_t slab,
-                                                        int64_t rows, int64_t dim, int64_t ld,
-                                                        unsigned short* __restrict__ out, int64_t out_stride) {
-    typedef u32x2 quad __attribute__((aligned(2)));
-    const int64_t quads = ld / 4;
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < rows * quads;
-         at += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = at / quads, d = (at - r * quads) * 4;
-        if (d >= dim) continue;
-        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-        for (int s = 0; s < n_slabs; ++s) x += *reinterpret_cast<const f32x4*>(slabs + s * slab + r * ld + d);
-        unsigned short* o = out + r * out_stride + d;
-        if (d + 4 <= dim) {
-            *reinterpret_cast<quad*>(o) = u32x2{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])};
-        } else {
-            #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (d + e < dim) o[e] = pack1<DT>(x[e]);
+__global__ __launch_bounds__(256) void prepare_kernel(const Prepare q) {
+    const uint32_t block = blockIdx.x;
+    if (block < q.ends[0]) {
+        column_sums<DT>(q, block);
+    } else if (block < q.ends[1]) {
+        write_held<DT>(q.held[0], block - q.ends[0]);
+    } else if (block < q.ends[2]) {
+        write_held<DT>(q.held[1], block - q.ends[1]);
+    } else {
+        const int64_t pieces = q.dyr_ld / 8, blocks = q.ends[3] - q.ends[2];
+        for (int64_t at = static_cast<int64_t>(block - q.ends[2]) * 256 + threadIdx.x; at < q.tokens * pieces;
+             at += blocks * 256) {
+            const int64_t r = at / pieces, d = (at - r * pieces) * 8;
+            *reinterpret_cast<u32x4*>(q.dyr + r * q.dyr_ld + d) = row_piece(q.dy + r * q.dy_stride, d, q.out);
         }
+    }
+}
+
+// What is left of results cut into parts: slices of dx and of dw, shares of
+// db, each joined in order, one launch.
+struct Slabs {
+    const float* slabs;
+    int64_t slab, rows, ld;
+    int32_t slices, wide;     // columns
+    unsigned short* out;
+    int64_t out_stride;
+};
+struct Finish {
+    Slabs of[2];
+    const float* part;
+    int64_t out;
+    int32_t shares;
+    unsigned short* db;
+    uint32_t ends[3];
+};
+template <int DT>
+__global__ __launch_bounds__(256) void finish_kernel(const Finish q) {
+    typedef u32x2 quad __attribute__((aligned(2)));
+    const uint32_t block = blockIdx.x;
+    if (block >= q.ends[1]) {
+        const int64_t n = static_cast<int64_t>(block - q.ends[1]) * 256 + threadIdx.x;
+        if (n >= q.out) return;
+        float total = 0.0f;
+        for (int i = 0; i < q.shares; ++i) total += q.part[i * q.out + n];
+        q.db[n] = pack1<DT>(total);
+        return;
+    }
+    const Slabs& b = q.of[block >= q.ends[0]];
+    const int64_t quads = b.ld / 4, at = static_cast<int64_t>(block - (block >= q.ends[0] ? q.ends[0] : 0)) * 256 + threadIdx.x;
+    const int64_t r = at / quads, d = (at - r * quads) * 4;
+    if (r >= b.rows || d >= b.wide) return;
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < b.slices; ++s) x += *reinterpret_cast<const f32x4*>(b.slabs + s * b.slab + r * b.ld + d);
+    unsigned short* o = b.out + r * b.out_stride + d;
+    if (d + 4 <= b.wide) {
+        *reinterpret_cast<quad*>(o) = u32x2{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])};
+    } else {
+        #pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (d + e < b.wide) o[e] = pack1<DT>(x[e]);
     }
 }
 
 // ------------------------------------------------------------------ launches
 constexpr int64_t kMaxTokens = int64_t(1) << 20, kMaxOut = int64_t(1) << 20;
-constexpr int64_t kFewTokens = 64;            // few8_kernel's rule
+// few8_kernel's rule, and its 16 rows by 64 tokens that the CUs take in two
+// rounds.  Microseconds, and those of the tiles: 17 tokens x 4096 x 4096 6.9
+// and 22, x 16384 16.2 and 24.5; 64 x 4096 x 16384 22.9 and 25.1, x 1000 x 10007
+// 9.4 and 9.9; beyond 64, 128 x 4096 x 4096 (512 of those) 13.4 and 22.8, 512 x
+// 512 x 512 (256) 4.5 and 6.3, but 192 x 4096 x 4096 (768) 28.5 and 22.7, 128 x
+// 4096 x 16384 (2048) 40 and 25.6.
+constexpr int64_t kFewTokens = 64, kFewParts = 512;
+constexpr int kTilesAtOnce = 2 * kCus;        // of 128 x 128
+constexpr int64_t kMostPacks = 1 << 22;       // blocks; with the others' the grid's 32 bits hold them
 constexpr size_t kPieceBytes = size_t(512) << 20;
 
 // How a gradient is cut: by the three sizes alone.
@@ -175,7 +341,7 @@ struct Cut {
     int64_t piece;            // columns of dim at a time, a multiple of 256
     int32_t dx_slices, dw_slices;
     int32_t shares;           // of db's sum
-    size_t x_bytes, w_bytes, dy_bytes, slab_bytes, part_bytes;
+    size_t x_bytes, w_bytes, dy_bytes, dx_slab, dw_slab, part_bytes;
     size_t total;
 };
 
@@ -188,7 +354,7 @@ bool cut(int64_t tokens, int64_t dim, int64_t out, Cut* c) {
     // slices of the sum where the tiles of 128 x 128 alone would leave CUs idle
     const int64_t dim_tiles = c->piece / 128;
     auto slices = [](int64_t tiles, int64_t sum) {
-        int64_t s = 512 / tiles;
+        int64_t s = kTilesAtOnce / tiles;
         if (s > sum / 512) s = sum / 512;
         return static_cast<int32_t>(s < 1 ? 1 : (s > 64 ? 64 : s));
     };
@@ -201,18 +367,30 @@ bool cut(int64_t tokens, int64_t dim, int64_t out, Cut* c) {
     c->x_bytes = round_up(static_cast<size_t>(t * c->piece) * 2, 256);
     c->w_bytes = round_up(static_cast<size_t>(n * c->piece) * 2, 256);
     c->dy_bytes = round_up(static_cast<size_t>(t * up(n, 64)) * 2, 256);
-    const size_t dx_slab = c->dx_slices > 1 ? static_cast<size_t>(c->dx_slices) * t * c->piece * 4 : 0;
-    const size_t dw_slab = c->dw_slices > 1 ? static_cast<size_t>(c->dw_slices) * n * c->piece * 4 : 0;
-    c->slab_bytes = round_up(dx_slab > dw_slab ? dx_slab : dw_slab, 256);
+    c->dx_slab = c->dx_slices > 1 ? round_up(static_cast<size_t>(c->dx_slices) * t * c->piece * 4, 256) : 0;
+    c->dw_slab = c->dw_slices > 1 ? round_up(static_cast<size_t>(c->dw_slices) * n * c->piece * 4, 256) : 0;
     c->part_bytes = round_up(static_cast<size_t>(c->shares) * n * 4, 256);
-    c->total = c->x_bytes + c->w_bytes + c->dy_bytes + c->slab_bytes + c->part_bytes;
+    c->total = c->x_bytes + c->w_bytes + c->dy_bytes + c->dx_slab + c->dw_slab + c->part_bytes;
     return true;
+}
+
+// As many blocks as the CUs' LDS holds at once, if they come round at most 16
+// times; a block's rows as many as another's.
+template <int OT, int NF>
+void few(const Few& q, hipStream_t st) {
+    constexpr int kLds = 3 * kFewWaves * (1 + NF) * 2048 + 2 * kFewWaves * NF * 1024 + kMostGroups * 128;
+    constexpr int most = kCus * (kLdsBytes / kLds);
+    const int rows = (q.out + 15) / 16, tokens = (q.tokens + 16 * NF - 1) / (16 * NF);
+    int times = (rows * tokens + most - 1) / most;
+    times = times < kMostGroups ? times : kMostGroups;
+    const int blocks = (rows + times - 1) / times;
+    hipLaunchKernelGGL((few8_kernel<OT, NF>), dim3(blocks, tokens), dim3(kFewWaves * 64), 0, st, q);
 }
 
 template <int OT>
 int forward(const zero_linear8_args* a, hipStream_t st) {
     const int64_t k = ZERO_ROWS8_BYTES(a->dim);
-    if (a->tokens <= kFewTokens) {
+    if (a->tokens <= kFewTokens || (a->out + 15) / 16 * ((a->tokens + 63) / 64) <= kFewParts) {
         Few q = {};
         q.w = static_cast<const char*>(a->w8);
         q.x = static_cast<const char*>(a->x8);
@@ -226,10 +404,9 @@ int forward(const zero_linear8_args* a, hipStream_t st) {
         q.bias = static_cast<const unsigned short*>(a->bias);
         q.y = static_cast<unsigned short*>(a->y);
         q.ldy = a->y_stride;
-        const dim3 grid(static_cast<unsigned>((a->out + 15) / 16));
-        if (a->tokens <= 16) hipLaunchKernelGGL((few8_kernel<OT, 1>), grid, dim3(256), 0, st, q);
-        else if (a->tokens <= 32) hipLaunchKernelGGL((few8_kernel<OT, 2>), grid, dim3(256), 0, st, q);
-        else hipLaunchKernelGGL((few8_kernel<OT, 4>), grid, dim3(256), 0, st, q);
+        if (a->tokens <= 16) few<OT, 1>(q, st);
+        else if (a->tokens <= 32) few<OT, 2>(q, st);
+        else few<OT, 4>(q, st);
         return launch_error("product kernel launch");
     }
     Product q = {};
@@ -250,78 +427,122 @@ int forward(const zero_linear8_args* a, hipStream_t st) {
     return launch_error("product kernel launch");
 }
 
-// C = A B over k, in slices where there are more than one.
-template <int DT, Layout LB>
-void gradient(Product q, int slices, int64_t rows, int64_t dim, float* slabs, int64_t ld, void* out, int64_t out_stride,
-              hipStream_t st) {
-    if (slices > 1) {
-        q.slice = static_cast<int32_t>(up(up(q.k, slices) / slices, kTileK));
-        q.c = reinterpret_cast<char*>(slabs);
-        q.ldc = ld;
-        q.slab = rows * ld;
-        // tiles times slices are at most 512 of 128 x 128, one round of the chip
-        launch_tiles<DT, kCols, LB, kPart, 128, 128, 2, 2>(q, slices, st);
-        hipLaunchKernelGGL((slice_sum_kernel<DT>), dim3(blocks_for(rows * (ld / 4))), dim3(256), 0, st, slabs, slices,
-                           q.slab, rows, dim, ld, static_cast<unsigned short*>(out), out_stride);
-        return;
+// A gradient's product: its slices' parts go to `slabs`, without slices its
+// result where it belongs.
+void place(Product* q, int slices, float* slabs, int64_t ld, int64_t rows, int64_t wide, void* out, int64_t out_stride) {
+    q->slices = slices;
+    q->slice = static_cast<int32_t>(up(up(q->k, slices) / slices, kTileK));
+    q->valid_m = static_cast<int32_t>(wide);
+    q->c = slices > 1 ? reinterpret_cast<char*>(slabs) : static_cast<char*>(out);
+    q->ldc = slices > 1 ? ld : out_stride;
+    q->slab = rows * ld;
+}
+
+// dx's and dw's tiles of 128 x 128 in one grid, either may have none: each
+// leaves CUs idle by itself (509 tokens x 1000 x 2053 in fp16 13 and 9 us one
+// after the other).  Where there are more than the CUs take at once, each gets
+// blocks by its share of the work.
+template <int DT>
+void two_products(Product a, Product b, hipStream_t st) {
+    a.tiles_m = (a.m + 127) / 128;
+    b.tiles_m = (b.m + 127) / 128;
+    const int64_t na = tiles_of(a, 128, 128) * a.slices, nb = tiles_of(b, 128, 128) * b.slices;
+    int64_t first = na, second = nb;
+    if (na + nb > kTilesAtOnce) {
+        const double wa = static_cast<double>(na) * (a.slice + kTileK), wb = static_cast<double>(nb) * (b.slice + kTileK);
+        first = na == 0 ? 0 : (nb == 0 ? kTilesAtOnce : static_cast<int64_t>(kTilesAtOnce * (wa / (wa + wb)) + 0.5));
+        if (na > 0 && first < 1) first = 1;
+        if (nb > 0 && first > kTilesAtOnce - 1) first = kTilesAtOnce - 1;
+        second = kTilesAtOnce - first;
+        if (first > na) first = na;
+        if (second > nb) second = nb;
     }
-    q.slice = static_cast<int32_t>(up(q.k, kTileK));
-    q.c = static_cast<char*>(out);
-    q.ldc = out_stride;
-    q.valid_m = static_cast<int32_t>(dim);
-    launch_product<DT, kCols, LB, kPlain>(q, 1, st);
+    hipLaunchKernelGGL((two_products_kernel<DT, kEither, 128, 128, 2, 2>), dim3(static_cast<unsigned>(first + second)),
+                       dim3(256), 0, st, a, b, static_cast<int>(first));
 }
 
 template <int DT>
 int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
     char* ws = static_cast<char*>(a->workspace);
-    char* x16 = ws;
-    char* w16 = x16 + c.x_bytes;
-    char* dyr = w16 + c.w_bytes;
-    float* slabs = reinterpret_cast<float*>(dyr + c.dy_bytes);
-    float* part = reinterpret_cast<float*>(dyr + c.dy_bytes + c.slab_bytes);
+    unsigned short* x16 = reinterpret_cast<unsigned short*>(ws);
+    unsigned short* w16 = reinterpret_cast<unsigned short*>(ws + c.x_bytes);
+    unsigned short* dyr = reinterpret_cast<unsigned short*>(ws + c.x_bytes + c.w_bytes);
+    float* dx_slab = reinterpret_cast<float*>(ws + c.x_bytes + c.w_bytes + c.dy_bytes);
+    float* dw_slab = dx_slab + c.dx_slab / 4;
+    float* part = dw_slab + c.dw_slab / 4;
     const int64_t t = a->tokens, n = a->out;
-    if (a->db && n > 0) {
-        const ColumnSum q = {static_cast<const unsigned short*>(a->dy), a->dy_stride, t, n,
-                             up(up(t, c.shares) / c.shares, 8), part};
-        const unsigned blocks = static_cast<unsigned>(up(n, 256) / 256);
-        hipLaunchKernelGGL((column_sum_kernel<DT>), dim3(blocks, c.shares), dim3(256), 0, st, q);
-        hipLaunchKernelGGL((column_join_kernel<DT>), dim3(blocks), dim3(256), 0, st, part, c.shares, n,
-                           static_cast<unsigned short*>(a->db));
-    }
-    const bool want_dx = a->dx && t > 0, want_dw = a->dw && n > 0;
-    if (a->dim == 0 || (!want_dx && !want_dw)) return launch_error("product gradient kernel launch");
-    // no row or no column: nothing of dy is read
-    Matrix dy = {dyr, 128, 0};
-    if (t > 0 && n > 0) dy = prepared(a->dy, a->dy_stride, 0, t, n, up(n, 64), dyr, st);
-    for (int64_t d = 0; d < a->dim; d += c.piece) {
+    const bool want_dx = a->dx && t > 0 && a->dim > 0, want_dw = a->dw && n > 0 && a->dim > 0, want_db = a->db && n > 0;
+    const bool whole = whole_pieces(a->dy, a->dy_stride, n), repack = !whole && t > 0 && n > 0 && (want_dx || want_dw);
+    const int64_t dyr_ld = up(n, 64);
+    const int64_t last = want_dx || want_dw ? a->dim : 1;   // db alone: once
+    for (int64_t d = 0; d < last; d += c.piece) {
         const int64_t wide = a->dim - d < c.piece ? a->dim - d : c.piece;
-        Product q = {};
-        q.lda = c.piece * 2;
-        q.m = static_cast<int32_t>(up(wide, 8));
-        q.b = dy.p;
-        q.ldb = dy.stride;
-        int rc;
+        Prepare p = {};
+        auto held = [&](Held* h, const void* codes, int64_t stride, const float* scale, int64_t rows,
+                        unsigned short* out) -> uint32_t {
+            *h = {static_cast<const char*>(codes) + d, stride, scale, rows, static_cast<int32_t>(wide),
+                  static_cast<int32_t>(up(wide, 8) / 8), out, c.piece};
+            return static_cast<uint32_t>((rows * h->pieces + 256 * kPrepPieces - 1) / (256 * kPrepPieces));
+        };
+        p.dy = static_cast<const unsigned short*>(a->dy);
+        p.dy_stride = a->dy_stride;
+        p.tokens = t;
+        p.out = n;
+        p.dyr = dyr;
+        p.dyr_ld = dyr_ld;
+        p.column_blocks = static_cast<int32_t>(up(n, 256) / 256);
+        p.share = up(up(t, c.shares) / c.shares, 8);
+        p.part = part;
+        p.db = c.shares == 1 ? static_cast<unsigned short*>(a->db) : nullptr;
+        p.ends[0] = d == 0 && want_db ? static_cast<uint32_t>(p.column_blocks * c.shares) : 0;
+        p.ends[1] = p.ends[0] + (want_dx ? held(&p.held[0], a->w8, a->w8_stride, a->w_scale, n, w16) : 0);
+        p.ends[2] = p.ends[1] + (want_dw ? held(&p.held[1], a->x8, a->x8_stride, a->x_scale, t, x16) : 0);
+        const int64_t packs = (t * (dyr_ld / 8) + 255) / 256;
+        p.ends[3] = p.ends[2] + (d == 0 && repack ? static_cast<uint32_t>(packs < kMostPacks ? packs : kMostPacks) : 0);
+        if (p.ends[3] > 0) hipLaunchKernelGGL((prepare_kernel<DT>), dim3(p.ends[3]), dim3(256), 0, st, p);
+
+        Finish f = {};
+        Product dx = {}, dw = {};
+        auto both = [&](Product* q, const unsigned short* held16) {
+            q->a = reinterpret_cast<const char*>(held16);
+            q->lda = c.piece * 2;
+            q->m = static_cast<int32_t>(up(wide, 8));
+            // no row or no column: nothing of dy is read
+            q->b = whole ? static_cast<const char*>(a->dy) : reinterpret_cast<const char*>(dyr);
+            q->ldb = (whole ? a->dy_stride : dyr_ld) * 2;
+        };
         if (want_dx) {
-            if ((rc = zero_rows8_decode(static_cast<const char*>(a->w8) + d, a->w8_stride, a->w_scale, n, wide, w16,
-                                        c.piece, DT, st)))
-                return rc;
-            q.a = w16;
-            q.n = static_cast<int32_t>(t);
-            q.k = static_cast<int32_t>(n);
-            gradient<DT, kRows>(q, c.dx_slices, t, wide, slabs, c.piece, static_cast<unsigned short*>(a->dx) + d,
-                                a->dx_stride, st);
+            unsigned short* out = static_cast<unsigned short*>(a->dx) + d;
+            both(&dx, w16);
+            dx.n = static_cast<int32_t>(t);
+            dx.k = static_cast<int32_t>(n);
+            place(&dx, c.dx_slices, dx_slab, c.piece, t, wide, out, a->dx_stride);
+            f.of[0] = {dx_slab, dx.slab, t, c.piece, c.dx_slices, static_cast<int32_t>(wide), out, a->dx_stride};
+            f.ends[0] = c.dx_slices > 1 ? static_cast<uint32_t>((t * (c.piece / 4) + 255) / 256) : 0;
         }
+        f.ends[1] = f.ends[0];
         if (want_dw) {
-            if ((rc = zero_rows8_decode(static_cast<const char*>(a->x8) + d, a->x8_stride, a->x_scale, t, wide, x16,
-                                        c.piece, DT, st)))
-                return rc;
-            q.a = x16;
-            q.n = static_cast<int32_t>(n);
-            q.k = static_cast<int32_t>(t);
-            gradient<DT, kCols>(q, c.dw_slices, n, wide, slabs, c.piece, static_cast<unsigned short*>(a->dw) + d,
-                                a->dw_stride, st);
+            unsigned short* out = static_cast<unsigned short*>(a->dw) + d;
+            both(&dw, x16);
+            dw.n = static_cast<int32_t>(n);
+            dw.k = static_cast<int32_t>(t);
+            place(&dw, c.dw_slices, dw_slab, c.piece, n, wide, out, a->dw_stride);
+            f.of[1] = {dw_slab, dw.slab, n, c.piece, c.dw_slices, static_cast<int32_t>(wide), out, a->dw_stride};
+            f.ends[1] += c.dw_slices > 1 ? static_cast<uint32_t>((n * (c.piece / 4) + 255) / 256) : 0;
         }
+        f.part = part;
+        f.out = n;
+        f.shares = c.shares;
+        f.db = static_cast<unsigned short*>(a->db);
+        f.ends[2] = f.ends[1] + (d == 0 && want_db && c.shares > 1 ? static_cast<uint32_t>((n + 255) / 256) : 0);
+        // more than one slice only where they are one round of the small tiles
+        const bool large_dx = want_dx && c.dx_slices == 1 && large_tiles(dx, 1);
+        const bool large_dw = want_dw && c.dw_slices == 1 && large_tiles(dw, 1);
+        if (large_dx) launch_tiles<DT, kCols, kRows, kPlain, 256, 256, 2, 2>(dx, 1, st);
+        if (large_dw) launch_tiles<DT, kCols, kCols, kPlain, 256, 256, 2, 2>(dw, 1, st);
+        if ((want_dx && !large_dx) || (want_dw && !large_dw))
+            two_products<DT>(large_dx ? Product{} : dx, large_dw ? Product{} : dw, st);
+        if (f.ends[2] > 0) hipLaunchKernelGGL((finish_kernel<DT>), dim3(f.ends[2]), dim3(256), 0, st, f);
     }
     return launch_error("product gradient kernel launch");
 }

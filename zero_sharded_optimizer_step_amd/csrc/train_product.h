@@ -1,7 +1,6 @@
 // train_product.h -- the tiled matrix product of the training operators, its
-// operands' layouts and epilogues, and what their sources share around it:
-// rows made whole for it, sums of slices, the choice of the tile.  Not part
-// of the public ABI.
+// operands' layouts and epilogues, and the choice of the tile.  Not part of
+// the public ABI.
 //
 // An operand lies with its rows along k (x and w in the loss's logits, P in
 // its dx) or with k as the row (w in dx; x and P in dw); the second kind is
@@ -39,8 +38,8 @@ enum Epilogue {
     kProb,      // P, 16 bits
     kSlab,      // fp32 partial products of one slice of k
     kGrad,      // the product times a factor, 16 bits
-    kPart,      // as kSlab, written over; of all n and k
-    kPlain,     // the product, 16 bits
+    kPlain,     // the product of all n and k, 16 bits
+    kEither,    // that; of more than one slice each one's fp32 part
     // of 8-bit codes: whole sums times both rows' scales, and a bias
     kScaledFp16,
     kScaledBf16
@@ -264,19 +263,18 @@ __device__ __forceinline__ bool infinite(float x) { return __builtin_fabsf(x) ==
 //   - blocks that stay: a tile's first loads run under the epilogue of the
 //     tile before (as separate blocks, and with an epilogue that spilled
 //     registers: 3.10 ms).
+// s0 to s4 are the five slots; the caller's, so that one kernel may hold two
+// products.  This block is `block` of `grid`.
+template <int BM, int BN>
+constexpr int kProductSlot = (BM > BN ? BM : BN) * kTileK * 2;
 template <int DT, Layout LA, Layout LB, Epilogue E, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) {
+__device__ __forceinline__ void product(const Product& q, int block, int grid, char* s0, char* s1, char* s2, char* s3,
+                                        char* s4) {
     constexpr int kThreads = WM * WN * 64;
     constexpr int FM = BM / WM / 16, FN = BN / WN / 16;     // fragments of a wave
     static_assert(FM % 2 == 0 && FN >= 4, "the epilogues' pairs and shares");
     typedef Operand<LA, BM, kThreads> OpA;
     typedef Operand<LB, BN, kThreads> OpB;
-    constexpr int kSlot = (BM > BN ? BM : BN) * kTileK * 2;
-    __shared__ __attribute__((aligned(1024))) char s0[kSlot];
-    __shared__ __attribute__((aligned(1024))) char s1[kSlot];
-    __shared__ __attribute__((aligned(1024))) char s2[kSlot];
-    __shared__ __attribute__((aligned(1024))) char s3[kSlot];
-    __shared__ __attribute__((aligned(1024))) char s4[kSlot];
 
     // The grid is what the chip holds at once; a block walks the tiles of all
     // slices.
@@ -288,7 +286,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
     const int size_n = kTokensAreN ? *q.kept : q.n, size_k = kTokensAreK ? *q.kept : q.k;
     const int tiles_n = (size_n + BN - 1) / BN;
     const int tiles = q.tiles_m * tiles_n, total = tiles * q.slices;
-    if (static_cast<int>(blockIdx.x) >= total) return;
+    if (block >= total) return;
     struct Place {
         int tm, m0, n0, slice, k_lo, k;                    // k: this slice's
     };
@@ -399,7 +397,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
     // The epilogues' code is kept short: it runs once a tile, and straight-line
     // code past the instruction cache costs more to fetch than to run.
     auto epilogue = [&](int tm, int m0, int n0, int slice, const int64_t (&target)[FN], const float (&lse)[FN],
-                        bool more) __attribute__((always_inline)) -> void {
+                        const f32x4 (&by)[FM], bool more) __attribute__((always_inline)) -> void {
         // the next tile's first loads, a share with each of the first four columns
         auto columns = [&](auto column) __attribute__((always_inline)) -> void {
             each<FN>([&](auto index) __attribute__((always_inline)) -> void {
@@ -519,7 +517,7 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 }
             };
             split(column);
-        } else if constexpr (E == kSlab || E == kPart) {
+        } else if (E == kSlab || (E == kEither && q.slices > 1)) {
             float* c = reinterpret_cast<float*>(q.c) + static_cast<int64_t>(slice) * q.slab;
             columns([&](auto index) __attribute__((always_inline)) -> void {
                 constexpr int j = decltype(index)::value;
@@ -540,33 +538,32 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                     if (n < size_n && i * 16 < end) row[i * 4] = x;
                 }
             });
-        } else {
+        } else if constexpr (E != kSlab) {
             float f = 1.0f;
             if constexpr (E == kGrad) f = q.scale * q.result->inv_count;
             typedef u32x4 eight __attribute__((aligned(2)));
-            // of the lane's m; past the last m the descriptors give 0
-            [[maybe_unused]] f32x4 by[FM], plus[FM];
+            // 16 rows of a wave's m, each 16 bytes longer, so that a column of them meets all banks
+            constexpr int kRoomRow = FM * 32 + 16, kRoomLanes = FM * 2;
+            static_assert(16 * kRoomRow * WM * WN <= kProductSlot<BM, BN>, "a slot holds the waves' rows");
+            ZERO_LDS char* room = (ZERO_LDS char*)s4 + wave * 16 * kRoomRow;
+            // of the lane's m; past the last m the descriptor gives 0
+            [[maybe_unused]] f32x4 plus[FM];
             if constexpr (kScaled) {
-                const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-                    const_cast<float*>(q.scale_m), 0, q.m * 4, 0x00020000);
                 const __amdgpu_buffer_rsrc_t rb = __builtin_amdgcn_make_buffer_rsrc(
                     const_cast<unsigned short*>(q.bias), 0, q.m * 2, 0x00020000);
                 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
-                    const int m = m0 + wm + i * 16 + ml;
-                    by[i] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, m * 4, 0, 0));
                     plus[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                     if (q.bias) {
                         #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            plus[i][e] = lo_to_f32<OT>(__builtin_amdgcn_raw_buffer_load_b16(rb, (m + e) * 2, 0, 0));
+                            plus[i][e] = lo_to_f32<OT>(
+                                __builtin_amdgcn_raw_buffer_load_b16(rb, (m0 + wm + i * 16 + ml + e) * 2, 0, 0));
                     }
                 }
             }
             columns([&](auto index) __attribute__((always_inline)) -> void {
                 constexpr int j = decltype(index)::value;
-                const int n = n0 + wn + j * 16 + nl;
-                unsigned short* row = reinterpret_cast<unsigned short*>(q.c) + n * q.ldc;
                 // an accumulator as it is written; a whole sum is rounded to fp32 first
                 auto result = [&](int i) __attribute__((always_inline)) -> f32x4 {
                     f32x4 x = taken(acc[i][j]);
@@ -577,10 +574,20 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                     }
                     return x;
                 };
+                // A lane has 4 of m in 16 rows of m apart; stored so, every lane is an
+                // address of its own.  Turned by way of the free slot, 16 bytes a lane
+                // lie one behind the other along a row.
                 #pragma unroll
-                for (int i = 0; i < FM; i += 2) {
-                    const u32x4 o = pair<OT>(result(i), result(i + 1), f);
-                    const int m = m0 + wm + i * 16 + pair_m;
+                for (int i = 0; i < FM; ++i) {
+                    const f32x4 x = result(i);
+                    *(ZERO_LDS u32x2*)(room + nl * kRoomRow + i * 32 + ml * 2) =
+                        u32x2{pack2<OT>(x[0] * f, x[1] * f), pack2<OT>(x[2] * f, x[3] * f)};
+                }
+                #pragma unroll
+                for (int r = lane / kRoomLanes; r < 16; r += 64 / kRoomLanes) {
+                    const u32x4 o = *(const ZERO_LDS u32x4*)(room + r * kRoomRow + lane % kRoomLanes * 16);
+                    const int n = n0 + wn + j * 16 + r, m = m0 + wm + lane % kRoomLanes * 8;
+                    unsigned short* row = reinterpret_cast<unsigned short*>(q.c) + n * q.ldc;
                     if (n >= size_n || m >= q.valid_m) continue;
                     if (m + 8 <= q.valid_m) {
                         *reinterpret_cast<eight*>(row + m) = o;
@@ -594,10 +601,10 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
         }
     };
 
-    begin(blockIdx.x);
+    begin(block);
     #pragma unroll
     for (int g = 0; g < 4; ++g) first_loads(g);
-    for (int id = blockIdx.x;;) {
+    for (int id = block;;) {
         #pragma unroll
         for (int i = 0; i < FM; ++i)
             #pragma unroll
@@ -621,6 +628,15 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
                 if constexpr (kScaled) lse[j] = q.scale_n[n < size_n ? n : size_n - 1];   // the row's scale
             }
         }
+        [[maybe_unused]] f32x4 by[FM];                     // the scales of the lane's m
+        if constexpr (kScaled) {
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                const_cast<float*>(q.scale_m), 0, q.m * 4, 0x00020000);
+            #pragma unroll
+            for (int i = 0; i < FM; ++i)
+                by[i] = __builtin_bit_cast(
+                    f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (w.m0 + wm + i * 16 + ml) * 4, 0, 0));
+        }
         #pragma unroll
         for (int x = 0; x < FM + FN; ++x) read(f0, s0, s1, at_a, at_b, 0, x);
         const int steps = (w.k + kTileK - 1) / kTileK;
@@ -637,64 +653,39 @@ __global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) 
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         const int tm = w.tm, m0 = w.m0, n0 = w.n0, slice = w.slice;
-        id += gridDim.x;
+        id += grid;
         if (id < total) begin(id);
-        epilogue(tm, m0, n0, slice, target, lse, id < total);
+        epilogue(tm, m0, n0, slice, target, lse, by, id < total);
         if (id >= total) break;
     }
 }
 
-// The slabs' sum times the factor, 16 bits; slabs in order.  With `rank` a
-// row's sum is in row rank[r], and 0 where that is negative.
-template <int DT>
-__global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__ slabs, int n_slabs, int64_t slab,
-                                                       int64_t rows, int64_t dim, int64_t ld,
-                                                       const zero_xent_result_t* __restrict__ result, float scale,
-                                                       const int32_t* __restrict__ rank,
-                                                       unsigned short* __restrict__ out, int64_t out_stride) {
-    typedef u32x2 quad __attribute__((aligned(2)));
-    const int64_t quads = ld / 4;
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < rows * quads;
-         at += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = at / quads, d = (at - r * quads) * 4;
-        if (d >= dim) continue;
-        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
-        const int64_t from = rank ? rank[r] : r;
-        for (int s = 0; s < (from < 0 ? 0 : n_slabs); ++s) {
-            const f32x4 y = *reinterpret_cast<const f32x4*>(slabs + s * slab + from * ld + d);
-            #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] += y[e];
-        }
-        const float f = scale * result->inv_count;
-        unsigned short* o = out + r * out_stride + d;
-        if (d + 4 <= dim) {
-            u32x2 v;
-            v.x = pack2<DT>(x[0] * f, x[1] * f);
-            v.y = pack2<DT>(x[2] * f, x[3] * f);
-            *reinterpret_cast<quad*>(o) = v;
-        } else {
-            #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (d + e < dim) o[e] = pack1<DT>(x[e] * f);
-        }
-    }
+template <int DT, Layout LA, Layout LB, Epilogue E, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64) void product_kernel(const Product q) {
+    constexpr int kSlot = kProductSlot<BM, BN>;
+    __shared__ __attribute__((aligned(1024))) char s0[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s1[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s2[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s3[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s4[kSlot];
+    product<DT, LA, LB, E, BM, BN, WM, WN>(q, blockIdx.x, gridDim.x, s0, s1, s2, s3, s4);
 }
 
-// Rows of any stride and alignment into rows of ld elements (a multiple of
-// 64), zeros past dim: what the products read where the caller's rows are
-// not whole 16-byte pieces.
-__global__ __launch_bounds__(256) void repack_kernel(const unsigned short* __restrict__ src, int64_t stride,
-                                                     int64_t rows, int64_t dim, int64_t ld,
-                                                     unsigned short* __restrict__ dst) {
-    const int64_t pieces = ld / 8;
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < rows * pieces;
-         at += static_cast<int64_t>(gridDim.x) * 256) {
-        const int64_t r = at / pieces, d = (at - r * pieces) * 8;
-        *reinterpret_cast<u32x4*>(dst + r * ld + d) = row_piece(src + r * stride, d, dim);
-    }
+// Two products that share B's rows' memory but not the way it is read, as one
+// grid: the first `first` blocks walk one's tiles, the others the other's.
+template <int DT, Epilogue E, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(WM * WN * 64) void two_products_kernel(const Product qa, const Product qb, int first) {
+    constexpr int kSlot = kProductSlot<BM, BN>;
+    __shared__ __attribute__((aligned(1024))) char s0[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s1[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s2[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s3[kSlot];
+    __shared__ __attribute__((aligned(1024))) char s4[kSlot];
+    const int block = blockIdx.x;
+    if (block < first) product<DT, kCols, kRows, E, BM, BN, WM, WN>(qa, block, first, s0, s1, s2, s3, s4);
+    else product<DT, kCols, kCols, E, BM, BN, WM, WN>(qb, block - first, gridDim.x - first, s0, s1, s2, s3, s4);
 }
 
-// ------------------------------------------------------------------ launches
 int launch_error(const char* what) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return fail(ZERO_EDEVICE, "%s: %s", what, hipGetErrorString(e));
@@ -702,12 +693,6 @@ int launch_error(const char* what) {
 }
 
 constexpr int64_t up(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
-
-// Blocks of 256 threads for n items, each walking the rest of the grid.
-unsigned blocks_for(int64_t n) {
-    const int64_t b = (n + 255) / 256;
-    return static_cast<unsigned>(b < (1 << 20) ? b : (1 << 20));
-}
 
 template <int DT, Layout LA, Layout LB, Epilogue E, int BM, int BN, int WM, int WN>
 void launch_tiles(Product q, int slices, hipStream_t st) {
@@ -750,29 +735,10 @@ void launch_product(const Product& q, int slices, hipStream_t st) {
     else launch_tiles<DT, LA, LB, E, 128, 128, 2, 2>(q, slices, st);
 }
 
-// One 16-bit matrix as the products read it: the caller's own rows where
-// they are whole 16-byte pieces, else rows repacked into the workspace.
+// Rows that the products read where they lie: whole 16-byte pieces.  Others
+// are copied first.
 bool whole_pieces(const void* p, int64_t stride, int64_t dim) {
     return aligned16(p) && stride % 8 == 0 && dim % 8 == 0 && stride <= (int64_t(1) << 21);
-}
-void launch_repack(const void* src, int64_t stride, int64_t rows, int64_t dim, int64_t ld, void* dst, hipStream_t st) {
-    const int64_t n = rows * (ld / 8);
-    hipLaunchKernelGGL(repack_kernel, dim3(blocks_for(n)), dim3(256), 0, st,
-                       static_cast<const unsigned short*>(src), stride, rows, dim, ld,
-                       static_cast<unsigned short*>(dst));
-}
-
-struct Matrix {
-    const char* p;
-    int64_t stride;           // bytes
-    int32_t dim;              // readable elements of a row, a multiple of 8
-};
-Matrix prepared(const void* src, int64_t stride, int64_t first, int64_t rows, int64_t dim, int64_t dim_pad,
-                void* room, hipStream_t st) {
-    const unsigned short* at = static_cast<const unsigned short*>(src) + first * stride;
-    if (whole_pieces(src, stride, dim)) return {reinterpret_cast<const char*>(at), stride * 2, static_cast<int32_t>(dim)};
-    launch_repack(at, stride, rows, dim, dim_pad, room, st);
-    return {static_cast<const char*>(room), dim_pad * 2, static_cast<int32_t>(dim_pad)};
 }
 
 }  // namespace

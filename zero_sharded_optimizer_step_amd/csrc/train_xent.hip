@@ -238,6 +238,57 @@ __global__ __launch_bounds__(1024) void xent_mean_kernel(const float* __restrict
     if (threadIdx.x == 0) write_mean(s_sum[0], s_count[0], s_beyond[0], out);
 }
 
+// The slabs' sum times the factor, 16 bits; slabs in order.  With `rank` a
+// row's sum is in row rank[r], and 0 where that is negative.
+template <int DT>
+__global__ __launch_bounds__(256) void slab_sum_kernel(const float* __restrict__ slabs, int n_slabs, int64_t slab,
+                                                       int64_t rows, int64_t dim, int64_t ld,
+                                                       const zero_xent_result_t* __restrict__ result, float scale,
+                                                       const int32_t* __restrict__ rank,
+                                                       unsigned short* __restrict__ out, int64_t out_stride) {
+    typedef u32x2 quad __attribute__((aligned(2)));
+    const int64_t quads = ld / 4;
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < rows * quads;
+         at += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = at / quads, d = (at - r * quads) * 4;
+        if (d >= dim) continue;
+        f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int64_t from = rank ? rank[r] : r;
+        for (int s = 0; s < (from < 0 ? 0 : n_slabs); ++s) {
+            const f32x4 y = *reinterpret_cast<const f32x4*>(slabs + s * slab + from * ld + d);
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] += y[e];
+        }
+        const float f = scale * result->inv_count;
+        unsigned short* o = out + r * out_stride + d;
+        if (d + 4 <= dim) {
+            u32x2 v;
+            v.x = pack2<DT>(x[0] * f, x[1] * f);
+            v.y = pack2<DT>(x[2] * f, x[3] * f);
+            *reinterpret_cast<quad*>(o) = v;
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (d + e < dim) o[e] = pack1<DT>(x[e] * f);
+        }
+    }
+}
+
+// Rows of any stride and alignment into rows of ld elements (a multiple of
+// 64), zeros past dim: what the products read where the caller's rows are
+// not whole 16-byte pieces.
+__global__ __launch_bounds__(256) void repack_kernel(const unsigned short* __restrict__ src, int64_t stride,
+                                                     int64_t rows, int64_t dim, int64_t ld,
+                                                     unsigned short* __restrict__ dst) {
+    const int64_t pieces = ld / 8;
+    for (int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; at < rows * pieces;
+         at += static_cast<int64_t>(gridDim.x) * 256) {
+        const int64_t r = at / pieces, d = (at - r * pieces) * 8;
+        *reinterpret_cast<u32x4*>(dst + r * ld + d) = row_piece(src + r * stride, d, dim);
+    }
+}
+
+// ------------------------------------------------------------------ launches
 // The tokens that have a target, one after another: their rows of x (as
 // repack_kernel lays them), targets and lse, how many they are, and every
 // token's place among them (-1: none).  The gradient's products then run
@@ -362,6 +413,34 @@ bool cut(int64_t tokens, int64_t dim, int64_t vocab, bool packed, Cut* c) {
     if (tokens > 0 && (dim < 1 || vocab < 1)) return false;
     cut_piece(tokens, dim, vocab, packed, c);
     return true;
+}
+
+// Blocks of 256 threads for n items, each walking the rest of the grid.
+unsigned blocks_for(int64_t n) {
+    const int64_t b = (n + 255) / 256;
+    return static_cast<unsigned>(b < (1 << 20) ? b : (1 << 20));
+}
+
+// One 16-bit matrix as the products read it: the caller's own rows where
+// they are whole 16-byte pieces, else rows repacked into the workspace.
+void launch_repack(const void* src, int64_t stride, int64_t rows, int64_t dim, int64_t ld, void* dst, hipStream_t st) {
+    const int64_t n = rows * (ld / 8);
+    hipLaunchKernelGGL(repack_kernel, dim3(blocks_for(n)), dim3(256), 0, st,
+                       static_cast<const unsigned short*>(src), stride, rows, dim, ld,
+                       static_cast<unsigned short*>(dst));
+}
+
+struct Matrix {
+    const char* p;
+    int64_t stride;           // bytes
+    int32_t dim;              // readable elements of a row, a multiple of 8
+};
+Matrix prepared(const void* src, int64_t stride, int64_t first, int64_t rows, int64_t dim, int64_t dim_pad,
+                void* room, hipStream_t st) {
+    const unsigned short* at = static_cast<const unsigned short*>(src) + first * stride;
+    if (whole_pieces(src, stride, dim)) return {reinterpret_cast<const char*>(at), stride * 2, static_cast<int32_t>(dim)};
+    launch_repack(at, stride, rows, dim, dim_pad, room, st);
+    return {static_cast<const char*>(room), dim_pad * 2, static_cast<int32_t>(dim_pad)};
 }
 
 template <int DT>

@@ -394,30 +394,58 @@ def _rows(name: str, t, rows: int, cols: int, dtype) -> int:
         raise ValueError("%s is %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != (rows, cols):
         raise ValueError("%s is %s, expected %s" % (name, tuple(t.shape), (rows, cols)))
-    s = t.stride()
-    if cols > 1 and rows > 0 and s[1] != 1:
+    stride, along = t.stride()
+    if along != 1 and cols > 1 and rows > 0:
         raise ValueError("%s's rows are not contiguous" % name)
     # a single row may carry any stride; the library wants cols or more
-    return s[0] if rows > 1 else max(s[0], cols)
+    return stride if rows > 1 else max(stride, cols)
 
 
 def _codes(name: str, t, scale, rows: int, dim: int) -> int:
     """The row stride of codes int8 [rows, rows8_stride(dim) or more]."""
     torch = _torch()
-    wide = rows8_stride(dim)
     if scale is None or t is None:
         raise ValueError("%s and its scale are given together" % name)
     if t.dtype != torch.int8:
         raise ValueError("%s is %s, expected torch.int8" % (name, t.dtype))
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] < wide:
-        raise ValueError("%s is %s, expected [%d, %d or more]" % (name, tuple(t.shape), rows, wide))
-    s = t.stride()
-    if wide > 0 and rows > 0 and s[1] != 1:
+    wide = (dim + 15) // 16 * 16
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] < wide:
+        raise ValueError("%s is %s, expected [%d, %d or more]" % (name, tuple(shape), rows, wide))
+    stride, along = t.stride()
+    if along != 1 and wide > 0 and rows > 0:
         raise ValueError("%s's rows are not contiguous" % name)
     if scale.dtype != torch.float32 or scale.numel() != rows or not scale.is_contiguous():
         raise ValueError("%s's scale must be %d contiguous float32 values" % (name, rows))
     # one row, or rows of nothing, may carry any stride, also none that is a multiple of 16
-    return s[0] if rows > 1 and wide > 0 else wide
+    return stride if rows > 1 and wide > 0 else wide
+
+
+_DTYPE_CODES = {}
+
+
+def _dtype(dtype) -> int:
+    """dtype_code, looked up."""
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
+        code = _DTYPE_CODES[dtype] = dtype_code(dtype)
+    return code
+
+
+def _one_device(given: dict) -> None:
+    """As _on_device; where all tensors say the same device's number, without
+    building what an error would show."""
+    first = None
+    for t in given.values():
+        if first is None:
+            first = t.get_device()
+            if first < 0:
+                break
+        elif t.get_device() != first:
+            break
+    else:
+        return
+    _on_device(**given)
 
 
 def zero_rows8_encode(x, codes, scale, stream=None) -> None:
@@ -427,9 +455,9 @@ def zero_rows8_encode(x, codes, scale, stream=None) -> None:
         raise ValueError("x is %s; expected [rows, dim]" % (tuple(x.shape),))
     rows, dim = x.shape
     xs, cs = _rows("x", x, rows, dim, x.dtype), _codes("codes", codes, scale, rows, dim)
-    _on_device(x=x, codes=codes, scale=scale)
+    _one_device({"x": x, "codes": codes, "scale": scale})
     _launching(x)
-    check(train_lib().zero_rows8_encode(x.data_ptr(), xs, dtype_code(x.dtype), rows, dim, codes.data_ptr(), cs,
+    check(train_lib().zero_rows8_encode(x.data_ptr(), xs, _dtype(x.dtype), rows, dim, codes.data_ptr(), cs,
                                         scale.data_ptr(), _stream(stream)), "zero_rows8_encode")
 
 
@@ -440,10 +468,10 @@ def zero_rows8_decode(codes, scale, y, stream=None) -> None:
         raise ValueError("y is %s; expected [rows, dim]" % (tuple(y.shape),))
     rows, dim = y.shape
     ys, cs = _rows("y", y, rows, dim, y.dtype), _codes("codes", codes, scale, rows, dim)
-    _on_device(y=y, codes=codes, scale=scale)
+    _one_device({"y": y, "codes": codes, "scale": scale})
     _launching(y)
     check(train_lib().zero_rows8_decode(codes.data_ptr(), cs, scale.data_ptr(), rows, dim, y.data_ptr(), ys,
-                                        dtype_code(y.dtype), _stream(stream)), "zero_rows8_decode")
+                                        _dtype(y.dtype), _stream(stream)), "zero_rows8_decode")
 
 
 # ------------------------------------------------------------- gated activation
@@ -480,29 +508,40 @@ class Glu8Args:
             raise ValueError("%s must be a tensor [tokens, width]" % ("dh" if backward else "gate"))
         if self.kind not in _GLU_KINDS:
             raise ValueError("kind is %r, expected one of %s" % (self.kind, sorted(_GLU_KINDS)))
-        t, w = first.shape
+        (t, w), dtype = first.shape, first.dtype
         a.tokens, a.width = t, w
-        a.dtype, a.kind = dtype_code(first.dtype), _GLU_KINDS[self.kind]
+        a.dtype, a.kind = _dtype(dtype), _GLU_KINDS[self.kind]
         given = {}
-        for name in ("dh", "dgate", "dup") if backward else ("gate", "up", "h"):
-            m = getattr(self, name)
-            if m is None:
-                continue
-            given[name] = m
-            setattr(a, name + "_stride", _rows(name, m, t, w, first.dtype))
-            setattr(a, name, m.data_ptr())
-        for name, scale in (("gate8", "gate_scale"), ("up8", "up_scale"), ("h8", "h_scale")):
-            codes, s = getattr(self, name), getattr(self, scale)
-            if codes is None and s is None or backward and name == "h8":
-                continue
-            setattr(a, name + "_stride", _codes(name, codes, s, t, w))
-            given[name], given[scale] = codes, s
-            setattr(a, name, codes.data_ptr())
-            setattr(a, scale, s.data_ptr())
-        for name in (("gate8", "dgate") if backward else ()):
-            if name not in given:
-                raise ValueError("the backward needs %s" % name)
-        _on_device(**given)
+        if backward:
+            if self.dgate is None or self.gate8 is None:
+                raise ValueError("the backward needs gate8 and dgate")
+            given["dh"], a.dh, a.dh_stride = first, first.data_ptr(), _rows("dh", first, t, w, dtype)
+            m = given["dgate"] = self.dgate
+            a.dgate, a.dgate_stride = m.data_ptr(), _rows("dgate", m, t, w, dtype)
+            m = self.dup
+            if m is not None:
+                given["dup"], a.dup, a.dup_stride = m, m.data_ptr(), _rows("dup", m, t, w, dtype)
+        else:
+            given["gate"], a.gate, a.gate_stride = first, first.data_ptr(), _rows("gate", first, t, w, dtype)
+            m = self.up
+            if m is not None:
+                given["up"], a.up, a.up_stride = m, m.data_ptr(), _rows("up", m, t, w, dtype)
+            m = self.h
+            if m is not None:
+                given["h"], a.h, a.h_stride = m, m.data_ptr(), _rows("h", m, t, w, dtype)
+            q, m = self.h8, self.h_scale
+            if q is not None or m is not None:
+                a.h8_stride = _codes("h8", q, m, t, w)
+                given["h8"], given["h_scale"], a.h8, a.h_scale = q, m, q.data_ptr(), m.data_ptr()
+        q, m = self.gate8, self.gate_scale
+        if q is not None or m is not None:
+            a.gate8_stride = _codes("gate8", q, m, t, w)
+            given["gate8"], given["gate_scale"], a.gate8, a.gate_scale = q, m, q.data_ptr(), m.data_ptr()
+        q, m = self.up8, self.up_scale
+        if q is not None or m is not None:
+            a.up8_stride = _codes("up8", q, m, t, w)
+            given["up8"], given["up_scale"], a.up8, a.up_scale = q, m, q.data_ptr(), m.data_ptr()
+        _one_device(given)
         return a
 
 
@@ -553,36 +592,40 @@ class Linear8Args:
         if first is None or first.dim() != 2:
             raise ValueError("%s must be a tensor [tokens, out]" % ("dy" if backward else "y"))
         (t, n), k, dtype = first.shape, self.dim, first.dtype
-        a.tokens, a.dim, a.out, a.dtype = t, k, n, dtype_code(dtype)
-        given = {"workspace": self.workspace}
-        for name, shape in ((("dy", (t, n)), ("dx", (t, k)), ("dw", (n, k))) if backward else (("y", (t, n)),)):
-            m = getattr(self, name)
-            if m is None:
-                continue
-            given[name] = m
-            setattr(a, name + "_stride", _rows(name, m, *shape, dtype))
-            setattr(a, name, m.data_ptr())
-        for name, scale, rows, used in (("x8", "x_scale", t, not backward or self.dw is not None),
-                                        ("w8", "w_scale", n, not backward or self.dx is not None)):
-            if not used:
-                continue
-            codes, s = getattr(self, name), getattr(self, scale)
-            setattr(a, name + "_stride", _codes(name, codes, s, rows, k))
-            given[name], given[scale] = codes, s
-            setattr(a, name, codes.data_ptr())
-            setattr(a, scale, s.data_ptr())
-        name = "db" if backward else "bias"
-        v = getattr(self, name)
+        a.tokens, a.dim, a.out, a.dtype = t, k, n, _dtype(dtype)
+        m = self.workspace
+        if not m.is_contiguous():
+            raise ValueError("workspace is not contiguous")
+        a.workspace, a.workspace_bytes = m.data_ptr(), m.numel() * m.element_size()
+        given = {"workspace": m}
+        if backward:
+            given["dy"], a.dy, a.dy_stride = first, first.data_ptr(), _rows("dy", first, t, n, dtype)
+            dx, dw = self.dx, self.dw
+            if dx is not None:
+                given["dx"], a.dx, a.dx_stride = dx, dx.data_ptr(), _rows("dx", dx, t, k, dtype)
+            if dw is not None:
+                given["dw"], a.dw, a.dw_stride = dw, dw.data_ptr(), _rows("dw", dw, n, k, dtype)
+            v, name = self.db, "db"
+        else:
+            given["y"], a.y, a.y_stride = first, first.data_ptr(), _rows("y", first, t, n, dtype)
+            v, name = self.bias, "bias"
         if v is not None:
             if v.dtype != dtype or v.numel() != n or not v.is_contiguous():
                 raise ValueError("%s must be %d contiguous %s values" % (name, n, dtype))
             given[name] = v
-            setattr(a, name, v.data_ptr())
-        if not self.workspace.is_contiguous():
-            raise ValueError("workspace is not contiguous")
-        _on_device(**given)
-        a.workspace = self.workspace.data_ptr()
-        a.workspace_bytes = self.workspace.numel() * self.workspace.element_size()
+            if backward:
+                a.db = v.data_ptr()
+            else:
+                a.bias = v.data_ptr()
+        if not backward or dw is not None:
+            q, m = self.x8, self.x_scale
+            a.x8_stride = _codes("x8", q, m, t, k)
+            given["x8"], given["x_scale"], a.x8, a.x_scale = q, m, q.data_ptr(), m.data_ptr()
+        if not backward or dx is not None:
+            q, m = self.w8, self.w_scale
+            a.w8_stride = _codes("w8", q, m, n, k)
+            given["w8"], given["w_scale"], a.w8, a.w_scale = q, m, q.data_ptr(), m.data_ptr()
+        _one_device(given)
         return a
 
 
