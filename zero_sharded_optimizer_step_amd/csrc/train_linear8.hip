@@ -245,10 +245,10 @@ __device__ __forceinline__ void column_sums(const Prepare& q, uint32_t block) {
     if (q.out >= 8) add([&](const unsigned short* at) { return u32x4(*reinterpret_cast<const eight*>(at + d)); });
     else add([&](const unsigned short* at) { return row_piece(at, d, q.out); });
     // columns of two threads have the same sums twice
-    const int64_t place = d - static_cast<int64_t>(across) * 256;
+    const int64_t from = d - static_cast<int64_t>(across) * 256;
     #pragma unroll
     for (int e = 0; e < 8; ++e)
-        if (place + e >= 0) s_sum[row][place + e] = sum[e];
+        if (from + e >= 0) s_sum[row][from + e] = sum[e];
     __syncthreads();
     const int64_t n = static_cast<int64_t>(across) * 256 + threadIdx.x;
     if (n >= q.out) return;
@@ -303,6 +303,7 @@ __global__ __launch_bounds__(256) void finish_kernel(const Finish q) {
         const int64_t n = static_cast<int64_t>(block - q.ends[1]) * 256 + threadIdx.x;
         if (n >= q.out) return;
         float total = 0.0f;
+        #pragma unroll 8
         for (int i = 0; i < q.shares; ++i) total += q.part[i * q.out + n];
         q.db[n] = pack1<DT>(total);
         return;
@@ -312,6 +313,7 @@ __global__ __launch_bounds__(256) void finish_kernel(const Finish q) {
     const int64_t r = at / quads, d = (at - r * quads) * 4;
     if (r >= b.rows || d >= b.wide) return;
     f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    #pragma unroll 4
     for (int s = 0; s < b.slices; ++s) x += *reinterpret_cast<const f32x4*>(b.slabs + s * b.slab + r * b.ld + d);
     unsigned short* o = b.out + r * b.out_stride + d;
     if (d + 4 <= b.wide) {

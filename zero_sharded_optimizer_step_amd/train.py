@@ -448,6 +448,20 @@ def _one_device(given: dict) -> None:
     _on_device(**given)
 
 
+def _queue(t, stream):
+    """The handle of the stream that a call on t's device launches on; as
+    _launching and _stream."""
+    if stream is None:
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None and t.is_cuda:
+            device = torch.cuda.current_device()
+            if t.get_device() == device:
+                return raw(device)
+    _launching(t)
+    return _stream(stream)
+
+
 def zero_rows8_encode(x, codes, scale, stream=None) -> None:
     """Rows of x [rows, dim] (fp32, bf16 or fp16, any row stride) into codes
     int8 [rows, rows8_stride(dim) or more] and scale fp32 [rows]."""
@@ -456,9 +470,8 @@ def zero_rows8_encode(x, codes, scale, stream=None) -> None:
     rows, dim = x.shape
     xs, cs = _rows("x", x, rows, dim, x.dtype), _codes("codes", codes, scale, rows, dim)
     _one_device({"x": x, "codes": codes, "scale": scale})
-    _launching(x)
     check(train_lib().zero_rows8_encode(x.data_ptr(), xs, _dtype(x.dtype), rows, dim, codes.data_ptr(), cs,
-                                        scale.data_ptr(), _stream(stream)), "zero_rows8_encode")
+                                        scale.data_ptr(), _queue(x, stream)), "zero_rows8_encode")
 
 
 def zero_rows8_decode(codes, scale, y, stream=None) -> None:
@@ -469,9 +482,8 @@ def zero_rows8_decode(codes, scale, y, stream=None) -> None:
     rows, dim = y.shape
     ys, cs = _rows("y", y, rows, dim, y.dtype), _codes("codes", codes, scale, rows, dim)
     _one_device({"y": y, "codes": codes, "scale": scale})
-    _launching(y)
     check(train_lib().zero_rows8_decode(codes.data_ptr(), cs, scale.data_ptr(), rows, dim, y.data_ptr(), ys,
-                                        _dtype(y.dtype), _stream(stream)), "zero_rows8_decode")
+                                        _dtype(y.dtype), _queue(y, stream)), "zero_rows8_decode")
 
 
 # ------------------------------------------------------------- gated activation
@@ -548,15 +560,13 @@ class Glu8Args:
 def zero_glu8_forward(args: Glu8Args, stream=None) -> None:
     """h, h8 and the checkpoint of args, as far as they are given."""
     a = args.c_args(False)
-    _launching(args.gate)
-    check(train_lib().zero_glu8_forward(ctypes.byref(a), _stream(stream)), "zero_glu8_forward")
+    check(train_lib().zero_glu8_forward(ctypes.byref(a), _queue(args.gate, stream)), "zero_glu8_forward")
 
 
 def zero_glu8_backward(args: Glu8Args, stream=None) -> None:
     """dgate and dup of args from dh and the checkpoint."""
     a = args.c_args(True)
-    _launching(args.dh)
-    check(train_lib().zero_glu8_backward(ctypes.byref(a), _stream(stream)), "zero_glu8_backward")
+    check(train_lib().zero_glu8_backward(ctypes.byref(a), _queue(args.dh, stream)), "zero_glu8_backward")
 
 
 # ---------------------------------------------------------------- 8-bit products
@@ -632,12 +642,10 @@ class Linear8Args:
 def zero_linear8_forward(args: Linear8Args, stream=None) -> None:
     """y of args."""
     a = args.c_args(False)
-    _launching(args.y)
-    check(train_lib().zero_linear8_forward(ctypes.byref(a), _stream(stream)), "zero_linear8_forward")
+    check(train_lib().zero_linear8_forward(ctypes.byref(a), _queue(args.y, stream)), "zero_linear8_forward")
 
 
 def zero_linear8_backward(args: Linear8Args, stream=None) -> None:
     """Those of dx, dw and db of args that are given."""
     a = args.c_args(True)
-    _launching(args.dy)
-    check(train_lib().zero_linear8_backward(ctypes.byref(a), _stream(stream)), "zero_linear8_backward")
+    check(train_lib().zero_linear8_backward(ctypes.byref(a), _queue(args.dy, stream)), "zero_linear8_backward")
