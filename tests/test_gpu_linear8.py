@@ -98,6 +98,15 @@ def test_large_tiles(size):
     Call(*size, torch.bfloat16, bias=False).check()
 
 
+@pytest.mark.parametrize("size", [(700, 3000, 1501), (130, 5000, 3001), (1500, 4200, 260), (260, 16400, 515), (1100, 2100, 130)],
+                         ids=str)
+def test_sums_cut_into_slices(size):
+    """So few tiles and so long a sum that the forward's is cut too, with odd rows of the parts."""
+    say("linear8 slices %s" % (size,))
+    Call(*size, torch.bfloat16).check()
+    Call(*size, torch.float16, bias=False, pad=3, shift=1, any_codes=True).check()
+
+
 @pytest.mark.parametrize("pad,shift,code_pad", [(1, 0, 16), (3, 5, 0), (8, 8, 48)])
 def test_strides_and_alignment(pad, shift, code_pad):
     for size in ((5, 100, 70), (40, 65, 130), (200, 144, 260), (130, 1001, 140)):

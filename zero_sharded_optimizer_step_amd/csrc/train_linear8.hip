@@ -327,13 +327,14 @@ __global__ __launch_bounds__(256) void finish_kernel(const Finish q) {
 
 // ------------------------------------------------------------------ launches
 constexpr int64_t kMaxTokens = int64_t(1) << 20, kMaxOut = int64_t(1) << 20;
-// few8_kernel's rule, and its 16 rows by 64 tokens that the CUs take in two
-// rounds.  Microseconds, and those of the tiles: 17 tokens x 4096 x 4096 6.9
-// and 22, x 16384 16.2 and 24.5; 64 x 4096 x 16384 22.9 and 25.1, x 1000 x 10007
-// 9.4 and 9.9; beyond 64, 128 x 4096 x 4096 (512 of those) 13.4 and 22.8, 512 x
-// 512 x 512 (256) 4.5 and 6.3, but 192 x 4096 x 4096 (768) 28.5 and 22.7, 128 x
-// 4096 x 16384 (2048) 40 and 25.6.
-constexpr int64_t kFewTokens = 64, kFewParts = 512;
+// few8_kernel's rule: up to 64 tokens; up to 1024 while its parts, 16 rows by
+// 64 tokens, are at most two rounds of the CUs and dim is short.  Microseconds,
+// and those of the tiles: 17 tokens x 4096 x 4096 6.9 and 15, x 16384 16.2 and
+// 24.5; 64 x 4096 x 16384 22.9 and 25.1, x 1000 x 10007 9.4 and 9.9; 128 x 4096
+// x 4096 (512 parts) 13.6 and 15.7, 512 x 512 x 512 4.6 and 6.4, but 192 x 4096
+// x 4096 (768) 28.5 and 22.7, 128 x 16384 x 4096 38 and 32, 8000 x 4096 x 64 28.5
+// and 16.1.  It loses at 64 x 16384 x 1024, 18.9 and 14.2: few rows, long ones.
+constexpr int64_t kFewTokens = 64, kMoreTokens = 1024, kFewParts = 512, kFewDim = 4096;
 constexpr int kTilesAtOnce = 2 * kCus;        // of 128 x 128
 constexpr int64_t kMostPacks = 1 << 22;       // blocks; with the others' the grid's 32 bits hold them
 constexpr size_t kPieceBytes = size_t(512) << 20;
@@ -389,10 +390,74 @@ void few(const Few& q, hipStream_t st) {
     hipLaunchKernelGGL((few8_kernel<OT, NF>), dim3(blocks, tokens), dim3(kFewWaves * 64), 0, st, q);
 }
 
+// Slices of the forward's k: tiles that leave CUs idle take shares of it.  A
+// step of 128 of k takes a tile 0.53 us, all of their operands come at 10 TB/s
+// at best, a slice's sums are written and read once each, and joining them is
+// a launch.  Microseconds with 1, 2, 3, 4 and 8 slices, and the rule's choice:
+// 256 tokens x 4096 x 4096 23.0, 20.1, 18.7, 18.5, 23.0 (3); 256 x 16384 x 4096
+// 67.5, 46.6, 37.4, 40.2, 39.6 (3); 512 x 4096 x 4096 23.5, 24.6, 26.6, 27.3,
+// 43.9 (1); 700 x 8000 x 1500 43.3, 31.8, 26.4, 28.9, 32.8 (3).
+int forward_slices(int64_t tokens, int64_t dim, int64_t out) {
+    const int64_t tiles = up(tokens, 128) / 128 * (up(out, 128) / 128), steps = up(dim, 128) / 128;
+    const double operands = static_cast<double>(tiles) * 256.0 * static_cast<double>(dim) * 1e-7;
+    int best = 1;
+    double least = 1e300;
+    for (int s = 1; s <= 32 && s * tiles <= kTilesAtOnce && s <= steps; ++s) {
+        const double latency = 0.53 * static_cast<double>((steps + s - 1) / s);
+        const double join = s > 1 ? 3.0 + static_cast<double>(s * tokens) * static_cast<double>(out) * 1e-6 : 0.0;
+        const double t = (latency > operands ? latency : operands) + join;
+        if (t < least) {
+            least = t;
+            best = s;
+        }
+    }
+    return best;
+}
+bool few_rows(int64_t tokens, int64_t dim, int64_t out) {
+    if (tokens <= kFewTokens) return true;
+    return tokens <= kMoreTokens && dim <= kFewDim && (out + 15) / 16 * ((tokens + 63) / 64) <= kFewParts;
+}
+
+struct Join {
+    const int* slabs;
+    int64_t slab, ld;
+    int32_t slices, tokens, out;
+    const float *w_scale, *x_scale;
+    const unsigned short* bias;
+    unsigned short* y;
+    int64_t ldy;
+};
+// The slices' whole sums added, scaled and rounded; four channels a thread.
+template <int OT>
+__global__ __launch_bounds__(256) void join_kernel(const Join q) {
+    typedef u32x2 quad __attribute__((aligned(2)));
+    const int64_t quads = q.ld / 4, at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t n = at / quads, m = (at - n * quads) * 4;
+    if (n >= q.tokens || m >= q.out) return;
+    i32x4 sum = {0, 0, 0, 0};
+    #pragma unroll 4
+    for (int s = 0; s < q.slices; ++s) sum += *reinterpret_cast<const i32x4*>(q.slabs + s * q.slab + n * q.ld + m);
+    const float sx = q.x_scale[n];
+    float x[4];
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int64_t i = m + e < q.out ? m + e : q.out - 1;
+        x[e] = __builtin_fmaf(static_cast<float>(sum[e]) * sx, q.w_scale[i], q.bias ? lo_to_f32<OT>(q.bias[i]) : 0.0f);
+    }
+    unsigned short* o = q.y + n * q.ldy + m;
+    if (m + 4 <= q.out) {
+        *reinterpret_cast<quad*>(o) = u32x2{pack2<OT>(x[0], x[1]), pack2<OT>(x[2], x[3])};
+    } else {
+        #pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (m + e < q.out) o[e] = pack1<OT>(x[e]);
+    }
+}
+
 template <int OT>
 int forward(const zero_linear8_args* a, hipStream_t st) {
     const int64_t k = ZERO_ROWS8_BYTES(a->dim);
-    if (a->tokens <= kFewTokens || (a->out + 15) / 16 * ((a->tokens + 63) / 64) <= kFewParts) {
+    if (few_rows(a->tokens, a->dim, a->out)) {
         Few q = {};
         q.w = static_cast<const char*>(a->w8);
         q.x = static_cast<const char*>(a->x8);
@@ -411,6 +476,7 @@ int forward(const zero_linear8_args* a, hipStream_t st) {
         else few<OT, 4>(q, st);
         return launch_error("product kernel launch");
     }
+    constexpr Epilogue E = OT == ZERO_BF16 ? kScaledBf16 : kScaledFp16;
     Product q = {};
     q.a = static_cast<const char*>(a->w8);
     q.lda = a->w8_stride;
@@ -425,7 +491,19 @@ int forward(const zero_linear8_args* a, hipStream_t st) {
     q.scale_m = a->w_scale;
     q.scale_n = a->x_scale;
     q.bias = static_cast<const unsigned short*>(a->bias);
-    launch_product<kCodes, kRows, kRows, OT == ZERO_BF16 ? kScaledBf16 : kScaledFp16>(q, 1, st);
+    const int slices = forward_slices(a->tokens, a->dim, a->out);
+    if (slices == 1) {
+        launch_product<kCodes, kRows, kRows, E>(q, 1, st);
+        return launch_error("product kernel launch");
+    }
+    q.slice = static_cast<int32_t>(up(up(q.k, slices) / slices, kTileK));
+    q.c = static_cast<char*>(a->workspace);
+    q.ldc = up(a->out, 64);
+    q.slab = a->tokens * q.ldc;
+    launch_tiles<kCodes, kRows, kRows, E, 128, 128, 2, 2>(q, slices, st);
+    const Join j = {static_cast<const int*>(a->workspace), q.slab, q.ldc, slices, q.n, q.m, a->w_scale, a->x_scale,
+                    q.bias, static_cast<unsigned short*>(a->y), a->y_stride};
+    hipLaunchKernelGGL((join_kernel<OT>), dim3(static_cast<unsigned>((q.slab / 4 + 255) / 256)), dim3(256), 0, st, j);
     return launch_error("product kernel launch");
 }
 
@@ -558,7 +636,10 @@ extern "C" {
 
 size_t zero_linear8_workspace_bytes(int64_t tokens, int64_t dim, int64_t out) {
     Cut c;
-    return cut(tokens, dim, out, &c) ? c.total : 0;
+    if (!cut(tokens, dim, out, &c)) return 0;
+    const int slices = few_rows(tokens, dim, out) ? 1 : forward_slices(tokens, dim, out);
+    const size_t sums = slices > 1 ? static_cast<size_t>(slices) * tokens * up(out, 64) * 4 : 0;
+    return c.total > sums ? c.total : round_up(sums, 256);
 }
 
 int zero_linear8_forward(const zero_linear8_args* a, void* stream) {

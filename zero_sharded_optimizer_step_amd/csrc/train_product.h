@@ -40,7 +40,8 @@ enum Epilogue {
     kGrad,      // the product times a factor, 16 bits
     kPlain,     // the product of all n and k, 16 bits
     kEither,    // that; of more than one slice each one's fp32 part
-    // of 8-bit codes: whole sums times both rows' scales, and a bias
+    // of 8-bit codes: whole sums times both rows' scales, and a bias; of more
+    // than one slice each one's whole sums
     kScaledFp16,
     kScaledBf16
 };
@@ -517,7 +518,7 @@ __device__ __forceinline__ void product(const Product& q, int block, int grid, c
                 }
             };
             split(column);
-        } else if (E == kSlab || (E == kEither && q.slices > 1)) {
+        } else if (E == kSlab || ((E == kEither || kScaled) && q.slices > 1)) {
             float* c = reinterpret_cast<float*>(q.c) + static_cast<int64_t>(slice) * q.slab;
             columns([&](auto index) __attribute__((always_inline)) -> void {
                 constexpr int j = decltype(index)::value;
@@ -533,8 +534,10 @@ __device__ __forceinline__ void product(const Product& q, int block, int grid, c
                 #pragma unroll
                 for (int i = 0; i < FM; ++i) {
                     f32x4 x = taken(acc[i][j]);
-                    #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = y[i][e] + x[e];
+                    if constexpr (E == kSlab) {
+                        #pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = y[i][e] + x[e];
+                    }
                     if (n < size_n && i * 16 < end) row[i * 4] = x;
                 }
             });
