@@ -196,6 +196,7 @@ __device__ __forceinline__ void store_codes(const Piece<DT>& p, const Scale& k, 
 // has passed the barrier of the row between, as every reader had before it.
 template <int TR, int N>
 __device__ __forceinline__ void row_max(uint32_t (&t)[N], int turn) {
+    static_assert(TR <= 64 || TR >= 256, "a wave has whole rows, or a row the whole block");
     #pragma unroll
     for (int off = (TR < 64 ? TR : 64) / 2; off > 0; off >>= 1)
         #pragma unroll
@@ -480,8 +481,11 @@ unsigned row_blocks(int64_t rows, int64_t parts = 1) {
     return static_cast<unsigned>(b < most ? b : most);
 }
 
-// The threads and pieces of a row for the encoders, by its length.
-template <int DT, typename F>
+// The threads and pieces of a row for the encoders, by its length.  Of 16384
+// elements 512 threads hold two parts, gate and up (8192 rows forward 163 us;
+// 256, with 236 registers each, 175), and 256 one (4096 rows of gelu 64.5 us,
+// 512 72).
+template <int DT, int kParts, typename F>
 void by_row(int64_t dim, const F& f) {
     using std::integral_constant;
     constexpr int kMore = 8 / kPiece<DT>;
@@ -491,7 +495,7 @@ void by_row(int64_t dim, const F& f) {
     else if (eights <= 256) f(integral_constant<int, 64>{}, integral_constant<int, 4 * kMore>{}, std::true_type{});
     else if (eights <= 512) f(integral_constant<int, 256>{}, integral_constant<int, 2 * kMore>{}, std::true_type{});
     else if (eights <= 1024) f(integral_constant<int, 256>{}, integral_constant<int, 4 * kMore>{}, std::true_type{});
-    else if (eights <= 2048) f(integral_constant<int, 512>{}, integral_constant<int, 4 * kMore>{}, std::true_type{});
+    else if (eights <= 2048) f(integral_constant<int, 256 * kParts>{}, integral_constant<int, 8 / kParts * kMore>{}, std::true_type{});
     else f(integral_constant<int, 1024>{}, integral_constant<int, 4 * kMore>{}, std::false_type{});
 }
 // And for the readers, whose blocks take part of a row.
@@ -512,7 +516,7 @@ unsigned row_parts(int64_t dim) {
 
 template <int DT>
 void encode(const Encode& q, hipStream_t st) {
-    by_row<DT>(q.dim, [&](auto tr, auto p, auto held) {
+    by_row<DT, 1>(q.dim, [&](auto tr, auto p, auto held) {
         constexpr int TR = decltype(tr)::value, P = decltype(p)::value;
         hipLaunchKernelGGL((rows8_encode_kernel<DT, TR, P, decltype(held)::value>), dim3(row_blocks<TR>(q.rows)),
                            dim3(kThreads<TR>), 0, st, q);
@@ -531,7 +535,7 @@ void decode(Decode q, hipStream_t st) {
 
 template <int DT, int KIND, bool kGated>
 void glu_forward(const Glu& q, hipStream_t st) {
-    by_row<DT>(q.width, [&](auto tr, auto p, auto held) {
+    by_row<DT, kGated ? 2 : 1>(q.width, [&](auto tr, auto p, auto held) {
         constexpr int TR = decltype(tr)::value, P = decltype(p)::value;
         hipLaunchKernelGGL((glu8_forward_kernel<DT, KIND, kGated, TR, P, decltype(held)::value>),
                            dim3(row_blocks<TR>(q.tokens)), dim3(kThreads<TR>), 0, st, q);
