@@ -139,6 +139,40 @@ def test_sums_are_whole(tokens):
     c.check_forward()
 
 
+@pytest.mark.parametrize("size", [(1, 5, 3), (1, 513, 3000), (2, 1000, 4099), (2, 16, 70000), (3, 1027, 1100), (4, 3001, 400),
+                                  (5, 4100, 8200), (8, 600, 56000), (1, 131071, 65)], ids=str)
+def test_gradient_of_few_tokens(size):
+    """One pass over the weights.  A thread adds a quarter of a share's rows,
+    then four waves' and up to 512 shares' sums are joined 16 at once."""
+    t, k, n = size
+    say("linear8 few gradient %s" % (size,))
+    for dtype, pad, shift in ((torch.bfloat16, 0, 0), (torch.float16, 3, 1)):
+        c = Call(t, k, n, dtype, pad=pad, shift=shift, code_pad=16 * pad, any_codes=pad > 0)
+        Z.zero_linear8_backward(c.args)
+        dy = c.dy.double()
+        w = c.sixteen_bits(c.w8, c.ws)
+        shares = max(1, min(512, 1024 // -(-(-(-k // 256) * 256) // 512), n // 32))
+        chain = -(-n // shares) / 4 + 1 + 4 + shares / 16 + 16
+        dx, off = dy @ w, chain * ref.U * (dy.abs() @ w.abs())
+        ref.within(c.dx.double(), dx, off + ref.half_step(dx, dtype), "dx")
+        x = c.sixteen_bits(c.x8, c.xs)
+        dw, off = dy.t() @ x, t * ref.U * (dy.abs().t() @ x.abs())
+        ref.within(c.dw.double(), dw, off + ref.half_step(dw, dtype), "dw")
+        db, off = dy.sum(0), t * ref.U * dy.abs().sum(0)
+        ref.within(c.db.double(), db, off + ref.half_step(db, dtype), "db")
+        c.clean()
+        # each alone gives the same
+        for name in ("dx", "dw"):
+            kept = getattr(c, name).clone()
+            for other in {"dx", "dw", "db"} - {name}:
+                setattr(c.args, other, None)
+            getattr(c, name).fill_(-7)
+            Z.zero_linear8_backward(c.args)
+            assert torch.equal(getattr(c, name), kept), name
+            for other in ("dx", "dw", "db"):
+                setattr(c.args, other, getattr(c, other))
+
+
 @pytest.mark.parametrize("size", [(20, 90, 40), (200, 700, 300)], ids=str)
 def test_tokens_and_channels_that_are_not_finite(size):
     """A NaN scale is one token's or one channel's in y, that channel's share of every dx and that token's of every dw."""
@@ -289,7 +323,7 @@ def test_results_do_not_depend_on_the_run():
         assert all(torch.equal(a, b) for other in seen[1:] for a, b in zip(seen[0], other))
 
 
-@pytest.mark.parametrize("size", [(1, 700, 300), (40, 700, 300), (300, 700, 333)], ids=str)
+@pytest.mark.parametrize("size", [(1, 700, 300), (4, 1000, 2000), (40, 700, 300), (300, 700, 333)], ids=str)
 def test_captured_and_on_a_side_stream(size):
     say("linear8 captured %s" % (size,))
     c = Call(*size, torch.bfloat16)

@@ -7,7 +7,8 @@
 //   backward   x^ and w^ are written out in 16 bits (exact with the encoder's
 //              scales), as many columns of dim at a time as 512 MB hold; then
 //              dx = dy w^ and dw = dy^T x^.  Small results are cut along
-//              their sum into slices, joined in a fixed order.
+//              their sum into slices, joined in a fixed order.  Up to 8
+//              tokens one pass over w8's rows makes dw's beside dx's sums.
 #include "train_product.h"
 
 namespace zero {
@@ -325,6 +326,175 @@ __global__ __launch_bounds__(256) void finish_kernel(const Finish q) {
     }
 }
 
+// The gradient of up to 8 tokens: w8 is read once and dw written once, and
+// nothing else counts.  A wave takes rows of both, a thread 8 columns of them;
+// x^ and dx's sums of those columns stay in its registers, 64 rows' dy and
+// scales lie in LDS.  A block's four waves join their sums there; the shares
+// of the rows, up to 512, are joined 16 at once by a second kernel.
+struct FewGradient {
+    const char* w8;
+    const char* x8;
+    int64_t w_row, x_row;     // bytes
+    const float *w_scale, *x_scale;
+    const unsigned short* dy;
+    int64_t dy_stride;
+    int64_t out, dim, share;  // rows of a share
+    int32_t tokens;
+    float* part;              // [shares][tokens][ld], or NULL: no dx
+    int64_t ld;
+    unsigned short* dw;       // or NULL
+    int64_t dw_stride;
+    unsigned short* db;       // or NULL
+};
+constexpr int kFewColumns = 512;
+
+// Eight held values as 16 bits hold them.
+template <int DT>
+__device__ __forceinline__ void held8(const u32x2 c, float s, float o[8]) {
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const unsigned w = c[i / 2] >> (16 * (i % 2));
+        const unsigned h = pack2<DT>(static_cast<float>(static_cast<int8_t>(w)) * s,
+                                     static_cast<float>(static_cast<int8_t>(w >> 8)) * s);
+        o[2 * i] = lo_to_f32<DT>(h);
+        o[2 * i + 1] = hi_to_f32<DT>(h);
+    }
+}
+
+template <int DT, int T>
+__global__ __launch_bounds__(256) void few_gradient_kernel(const FewGradient q) {
+    constexpr int kRowsAtOnce = 64, kDeep = T > 4 ? 4 : 8; // rows of a block's turn; of a wave's whose loads go together
+    __shared__ float s_sum[4][kFewColumns];
+    __shared__ __attribute__((aligned(16))) float s_dy[kRowsAtOnce][T];
+    __shared__ float s_scale[kRowsAtOnce];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t d = static_cast<int64_t>(blockIdx.x) * kFewColumns + lane * 8;
+    const int64_t first = blockIdx.y * q.share, last = first + q.share < q.out ? first + q.share : q.out;
+    const bool in = d < q.dim;
+    const u32x2 none = {0u, 0u};
+    float x[T][8], sum[T][8];
+    #pragma unroll
+    for (int t = 0; t < T; ++t) {
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) x[t][e] = sum[t][e] = 0.0f;
+        if (q.dw && t < q.tokens)
+            held8<DT>(in ? *reinterpret_cast<const u32x2*>(q.x8 + t * q.x_row + d) : none, q.x_scale[t], x[t]);
+    }
+    for (int64_t base = first; base < last; base += kRowsAtOnce) {
+        const int rows = last - base < kRowsAtOnce ? static_cast<int>(last - base) : kRowsAtOnce;
+        __syncthreads();
+        for (int i = threadIdx.x; i < kRowsAtOnce * T; i += 256) {
+            const int row = i % kRowsAtOnce, t = i / kRowsAtOnce;
+            s_dy[row][t] = row < rows && t < q.tokens ? lo_to_f32<DT>(q.dy[t * q.dy_stride + base + row]) : 0.0f;
+        }
+        if (q.part && static_cast<int>(threadIdx.x) < rows) s_scale[threadIdx.x] = q.w_scale[base + threadIdx.x];
+        __syncthreads();
+        if (q.db && blockIdx.x == 0 && static_cast<int>(threadIdx.x) < rows) {
+            float all = 0.0f;
+            #pragma unroll
+            for (int t = 0; t < T; ++t) all += s_dy[threadIdx.x][t];
+            q.db[base + threadIdx.x] = pack1<DT>(all);
+        }
+        for (int r = wave; r < rows; r += 4 * kDeep) {
+            u32x2 c[kDeep];
+            #pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                const int64_t n = base + (r + 4 * i < rows ? r + 4 * i : r);
+                c[i] = q.part && in ? __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(q.w8 + n * q.w_row + d)) : none;
+            }
+            #pragma unroll
+            for (int i = 0; i < kDeep; ++i) {
+                const int row = r + 4 * i;
+                if (row >= rows) break;
+                // of tokens that there are not 0, as their x
+                float g[T];
+                #pragma unroll
+                for (int t = 0; t < T; ++t) g[t] = s_dy[row][t];
+                if (q.part) {
+                    float w[8];
+                    held8<DT>(c[i], s_scale[row], w);
+                    #pragma unroll
+                    for (int t = 0; t < T; ++t) {
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e) sum[t][e] = __builtin_fmaf(g[t], w[e], sum[t][e]);
+                    }
+                }
+                if (q.dw && in) {
+                    float o[8] = {};
+                    #pragma unroll
+                    for (int t = 0; t < T; ++t) {
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e) o[e] = __builtin_fmaf(g[t], x[t][e], o[e]);
+                    }
+                    const u32x4 v = {pack2<DT>(o[0], o[1]), pack2<DT>(o[2], o[3]), pack2<DT>(o[4], o[5]), pack2<DT>(o[6], o[7])};
+                    typedef u32x4 eight __attribute__((aligned(2)));
+                    unsigned short* to = q.dw + (base + row) * q.dw_stride + d;
+                    if (d + 8 <= q.dim) {
+                        __builtin_nontemporal_store(v, reinterpret_cast<eight*>(to));
+                    } else {
+                        #pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (d + e < q.dim) to[e] = static_cast<unsigned short>(v[e / 2] >> (16 * (e % 2)));
+                    }
+                }
+            }
+        }
+    }
+    if (!q.part) return;
+    float* part = q.part + static_cast<int64_t>(blockIdx.y) * q.tokens * q.ld;
+    #pragma unroll
+    for (int t = 0; t < T; ++t) {
+        if (t >= q.tokens) break;
+        __syncthreads();
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) s_sum[wave][lane * 8 + e] = sum[t][e];
+        __syncthreads();
+        #pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int at = e * 256 + threadIdx.x;
+            const int64_t column = static_cast<int64_t>(blockIdx.x) * kFewColumns + at;
+            if (column < q.ld) part[t * q.ld + column] = (s_sum[0][at] + s_sum[1][at]) + (s_sum[2][at] + s_sum[3][at]);
+        }
+    }
+}
+
+struct FewJoin {
+    const float* part;        // [shares][rows][ld]
+    int64_t ld;
+    int32_t shares, rows, dim;
+    unsigned short* out;
+    int64_t out_stride;
+};
+// Four columns of a row to 16 threads, each with every 16th share.
+template <int DT>
+__global__ __launch_bounds__(256) void few_join_kernel(const FewJoin q) {
+    typedef u32x2 quad __attribute__((aligned(2)));
+    __shared__ f32x4 s_sum[16][17];
+    const int mine = threadIdx.x % 16, group = threadIdx.x / 16;
+    const int64_t quads = q.ld / 4, at = static_cast<int64_t>(blockIdx.x) * 16 + mine;
+    const int64_t r = at / quads, d = (at - r * quads) * 4;
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (r < q.rows) {
+        #pragma unroll 8
+        for (int s = group; s < q.shares; s += 16)
+            x += *reinterpret_cast<const f32x4*>(q.part + (static_cast<int64_t>(s) * q.rows + r) * q.ld + d);
+    }
+    s_sum[group][mine] = x;
+    __syncthreads();
+    if (group != 0 || r >= q.rows || d >= q.dim) return;
+    #pragma unroll
+    for (int s = 1; s < 16; ++s) x += s_sum[s][mine];
+    unsigned short* o = q.out + r * q.out_stride + d;
+    if (d + 4 <= q.dim) {
+        *reinterpret_cast<quad*>(o) = u32x2{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])};
+    } else {
+        #pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (d + e < q.dim) o[e] = pack1<DT>(x[e]);
+    }
+}
+
 // ------------------------------------------------------------------ launches
 constexpr int64_t kMaxTokens = int64_t(1) << 20, kMaxOut = int64_t(1) << 20;
 // few8_kernel's rule: up to 64 tokens; up to 1024 while its parts, 16 rows by
@@ -345,8 +515,18 @@ struct Cut {
     int32_t dx_slices, dw_slices;
     int32_t shares;           // of db's sum
     size_t x_bytes, w_bytes, dy_bytes, dx_slab, dw_slab, part_bytes;
+    int32_t few_shares;       // few_gradient_kernel's
     size_t total;
 };
+
+// Whether few_gradient_kernel takes it.  Microseconds, and those of the tiles:
+// 1 token x 4096 x 16384 46 and 114, x 4096 15 and 36, x 64 x 64 7.3 and 7.9;
+// 4 tokens x 1000 x 2053 13 and 16, x 200 x 300 10.9 and 9.6; 8 tokens x 4096 x
+// 16384 95 and 114, x 512 x 100000 73 and 93, x 4096 x 4096 38 and 36.
+bool few_gradient_rule(int64_t tokens, int64_t dim, int64_t out) {
+    const int64_t weights = dim * out;
+    return tokens <= 2 || (tokens <= 4 && weights >= int64_t(1) << 20) || (tokens <= 8 && weights >= int64_t(1) << 25);
+}
 
 bool cut(int64_t tokens, int64_t dim, int64_t out, Cut* c) {
     if (tokens < 0 || tokens > kMaxTokens || dim < 0 || dim > ZERO_ROWS8_MAX_DIM || out < 0 || out > kMaxOut)
@@ -374,6 +554,13 @@ bool cut(int64_t tokens, int64_t dim, int64_t out, Cut* c) {
     c->dw_slab = c->dw_slices > 1 ? round_up(static_cast<size_t>(c->dw_slices) * n * c->piece * 4, 256) : 0;
     c->part_bytes = round_up(static_cast<size_t>(c->shares) * n * 4, 256);
     c->total = c->x_bytes + c->w_bytes + c->dy_bytes + c->dx_slab + c->dw_slab + c->part_bytes;
+    int64_t few = 1024 / (up(k, kFewColumns) / kFewColumns);
+    if (few > n / 32) few = n / 32;
+    c->few_shares = static_cast<int32_t>(few < 1 ? 1 : (few > 512 ? 512 : few));
+    if (few_gradient_rule(t, dim, n)) {
+        const size_t sums = round_up(static_cast<size_t>(c->few_shares) * t * up(k, 8) * 4, 256);
+        if (c->total < sums) c->total = sums;
+    }
     return true;
 }
 
@@ -542,7 +729,43 @@ void two_products(Product a, Product b, hipStream_t st) {
 }
 
 template <int DT>
+int few_gradient(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
+    FewGradient q = {};
+    q.w8 = static_cast<const char*>(a->w8);
+    q.x8 = static_cast<const char*>(a->x8);
+    q.w_row = a->w8_stride;
+    q.x_row = a->x8_stride;
+    q.w_scale = a->w_scale;
+    q.x_scale = a->x_scale;
+    q.dy = static_cast<const unsigned short*>(a->dy);
+    q.dy_stride = a->dy_stride;
+    q.out = a->out;
+    q.dim = a->dim;
+    q.share = up(up(a->out, c.few_shares) / c.few_shares, 4);
+    q.tokens = static_cast<int32_t>(a->tokens);
+    q.part = a->dx ? static_cast<float*>(a->workspace) : nullptr;
+    q.ld = up(a->dim, 8);
+    q.dw = static_cast<unsigned short*>(a->dw);
+    q.dw_stride = a->dw_stride;
+    q.db = static_cast<unsigned short*>(a->db);
+    const dim3 grid(static_cast<unsigned>(up(a->dim, kFewColumns) / kFewColumns), static_cast<unsigned>(c.few_shares));
+    if (a->tokens <= 1) hipLaunchKernelGGL((few_gradient_kernel<DT, 1>), grid, dim3(256), 0, st, q);
+    else if (a->tokens <= 2) hipLaunchKernelGGL((few_gradient_kernel<DT, 2>), grid, dim3(256), 0, st, q);
+    else if (a->tokens <= 4) hipLaunchKernelGGL((few_gradient_kernel<DT, 4>), grid, dim3(256), 0, st, q);
+    else hipLaunchKernelGGL((few_gradient_kernel<DT, 8>), grid, dim3(256), 0, st, q);
+    if (a->dx) {
+        const FewJoin j = {q.part, q.ld, c.few_shares, q.tokens, static_cast<int32_t>(a->dim),
+                           static_cast<unsigned short*>(a->dx), a->dx_stride};
+        hipLaunchKernelGGL((few_join_kernel<DT>), dim3(static_cast<unsigned>((a->tokens * (q.ld / 4) + 15) / 16)), dim3(256), 0,
+                           st, j);
+    }
+    return launch_error("product gradient kernel launch");
+}
+
+template <int DT>
 int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
+    if (a->tokens > 0 && a->dim > 0 && few_gradient_rule(a->tokens, a->dim, a->out) && (a->dx || (a->dw && a->out > 0)))
+        return few_gradient<DT>(a, c, st);
     char* ws = static_cast<char*>(a->workspace);
     unsigned short* x16 = reinterpret_cast<unsigned short*>(ws);
     unsigned short* w16 = reinterpret_cast<unsigned short*>(ws + c.x_bytes);
