@@ -260,7 +260,8 @@ int zero_xent_backward(const zero_xent_args* a, void* stream);
  *
  * A row of codes takes ZERO_ROWS8_BYTES(dim) bytes, dim rounded up to a
  * multiple of 16, and holds zeros from dim on; the encoder writes them.
- * Whoever makes codes by other means writes them too.  Rows start at
+ * Whoever makes codes by other means writes them too, and rows cut out of
+ * wider ones have them only where dim is a multiple of 16.  Rows start at
  * multiples of 16 bytes: 16-byte aligned, strides multiples of 16.  What
  * lies between a row's ZERO_ROWS8_BYTES and the next row is neither read nor
  * written.  The readers below take codes of [-128, 127] and any fp32 scale
@@ -273,13 +274,15 @@ int zero_xent_backward(const zero_xent_args* a, void* stream);
  * its element, x_stride (elements, >= dim, <= 2^31) from row to row.
  * rows in [0, 2^31), dim in [0, ZERO_ROWS8_MAX_DIM]; a row of no elements or
  * of zeros has the least scale.
+ * The codes and scales must not overlap x.
  * Errors: a size, stride or dtype out of range, a NULL pointer where there is
  * something to read or write -> ZERO_EINVAL; misalignment -> ZERO_EALIGN;
  * launch -> ZERO_EDEVICE. */
 int zero_rows8_encode(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, int64_t dim,
                       void* codes, int64_t codes_stride, float* scale, void* stream);
 
-/* The reverse: y = q s in fp32, rounded to nearest even to dtype. */
+/* The reverse: y = q s in fp32, rounded to nearest even to dtype.  y must not
+ * overlap the codes and scales.  Errors as above. */
 int zero_rows8_decode(const void* codes, int64_t codes_stride, const float* scale, int64_t rows,
                       int64_t dim, void* y, int64_t y_stride, int32_t dtype, void* stream);
 
@@ -377,8 +380,10 @@ typedef struct {
     size_t workspace_bytes;
 } zero_linear8_args;
 
-/* Bytes of workspace forward and backward need (one buffer serves both; no
- * call reads what another left there).  0 for out-of-range sizes.  Host only. */
+/* Bytes of workspace forward and backward need (one buffer serves both and
+ * all calls of these sizes that follow each other; no call reads what another
+ * left there; calls that overlap, on two streams or in two graphs, need one
+ * each).  0 for out-of-range sizes.  Host only. */
 size_t zero_linear8_workspace_bytes(int64_t tokens, int64_t dim, int64_t out);
 
 /* Writes y; dy, dx, dw and db are not used.  No output may overlap an input.

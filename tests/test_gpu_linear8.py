@@ -225,7 +225,7 @@ def test_only_what_is_wanted():
             assert torch.equal(kept[name], getattr(full, name)), name
 
 
-@pytest.mark.parametrize("size", [(0, 40, 30), (5, 0, 30), (100, 0, 30), (5, 40, 0), (0, 0, 0), (0, 0, 5), (3, 0, 0)], ids=str)
+@pytest.mark.parametrize("size", [(0, 40, 30), (5, 0, 30), (100, 0, 30), (5, 40, 0), (1, 40, 0), (2, 0, 30), (0, 0, 0), (0, 0, 5), (3, 0, 0)], ids=str)
 def test_empty_sizes(size):
     say("linear8 empty %s" % (size,))
     c = Call(*size, torch.bfloat16, pad=2)
@@ -279,9 +279,20 @@ def test_offsets_past_32_bits(tokens):
     y = torch.empty(tokens, out, dtype=torch.bfloat16, device="cuda")
     room = torch.empty(Z.zero_linear8_workspace_bytes(tokens, dim, out), dtype=torch.uint8, device="cuda")
     Z.zero_linear8_forward(Z.Linear8Args(x8, xs, w8, ws, dim=dim, workspace=room, y=y))
-    for rows in (slice(0, 300), slice((1 << 19) + 5, (1 << 19) + 3000), slice(out - 777, out)):
+    parts = (slice(0, 300), slice((1 << 19) + 5, (1 << 19) + 3000), slice(out - 777, out))
+    for rows in parts:
         want, off = ref.linear(x8, xs, w8[rows], ws[rows], dim, None)
         ref.within(y[:, rows].double(), want, off + ref.half_step(want, torch.bfloat16), "y")
+    dy = torch.randn(tokens, out, generator=g, device="cuda").to(torch.bfloat16)
+    dx = torch.empty(tokens, dim, dtype=torch.bfloat16, device="cuda")
+    dw = torch.empty(out, dim, dtype=torch.bfloat16, device="cuda")
+    Z.zero_linear8_backward(Z.Linear8Args(x8, xs, w8, ws, dim=dim, workspace=room, dy=dy, dx=dx, dw=dw))
+    cols = [0, 1, 255, 256, 511, 512, 3000, dim - 1]
+    want, off = ref.product(dy.double(), w8[:, cols].double() * 2.0**-9, out)
+    ref.within(dx[:, cols].double(), want, off + ref.half_step(want, torch.bfloat16), "dx")
+    for rows in parts:
+        want, off = ref.product(dy[:, rows].double().t(), x8.double() * 2.0**-9, tokens)
+        ref.within(dw[rows].double(), want, off + ref.half_step(want, torch.bfloat16), "dw")
 
 
 def test_gradient_against_differences():

@@ -2,8 +2,10 @@
 // gradient (include/zero/train.h).
 //
 //   forward    y = x8 w8^T in whole numbers on the matrix cores, scaled and
-//              rounded once in the epilogue.  Up to 64 tokens w8 goes straight
-//              from memory to registers.
+//              rounded once in the epilogue: by the tiles that the loss uses
+//              (8192 x 4096 x 16384 in 422 us, 2.6 POP/s, bound by the matrix
+//              cores' power), where they are few in slices of k; few tokens
+//              by a kernel whose waves need no barrier between their loads.
 //   backward   x^ and w^ are written out in 16 bits (exact with the encoder's
 //              scales), as many columns of dim at a time as 512 MB hold; then
 //              dx = dy w^ and dw = dy^T x^.  Small results are cut along
@@ -33,9 +35,9 @@ struct Few {
 // LDS.  The loads of the next rows are under way meanwhile.  They go to LDS
 // with 8 lanes along a row: as fragments straight into registers, a row to a
 // lane, every lane is an address of its own, and the 16 bytes a cycle and CU
-// that this gives bound the kernel (1 token x 4096 x 16384 15.7 us, 64 tokens
-// 46).  Blocks begin at unlike k, or all of them would meet in the same
-// channels of memory.
+// that this gives bound the kernel: 1 token x 4096 x 16384 took 15.7 us and 64
+// 46, now 11.6 (5.8 TB/s) and 23 to 28.  Blocks begin at unlike k, or all of
+// them would meet in the same channels of memory (1 token 17.4 and 15.7 then).
 constexpr int kFewWaves = 4, kMostGroups = 16;
 template <int OT, int NF>
 __global__ __launch_bounds__(kFewWaves * 64) void few8_kernel(const Few q) {
