@@ -267,6 +267,25 @@ def test_columns_in_pieces(size, dim_at):
     ref.within(dw[rows].double(), want, off + ref.half_step(want, torch.bfloat16), "dw")
 
 
+def test_more_of_dy_than_the_caches_hold():
+    t, k, n = 8209, 48, 16424
+    say("linear8 %d x %d x %d" % (t, k, n))
+    g = torch.Generator(device="cuda").manual_seed(0)
+    dy = torch.randn(t, n + 3, generator=g, device="cuda").to(torch.float16)[:, :n]
+    w = torch.randn(n, k, generator=g, device="cuda").to(torch.float16)
+    w8, ws = torch.empty(n, 48, dtype=torch.int8, device="cuda"), torch.empty(n, device="cuda")
+    Z.zero_rows8_encode(w, w8, ws)
+    Z.zero_rows8_decode(w8, ws, w)
+    dx, db = torch.empty(t, k, dtype=torch.float16, device="cuda"), torch.empty(n, dtype=torch.float16, device="cuda")
+    room = torch.empty(Z.zero_linear8_workspace_bytes(t, k, n), dtype=torch.uint8, device="cuda")
+    Z.zero_linear8_backward(Z.Linear8Args(None, None, w8, ws, dim=k, workspace=room, dy=dy, dx=dx, db=db))
+    want, off = ref.column_sum(dy, t)
+    ref.within(db.double(), want, off + ref.half_step(want, torch.float16), "db")
+    rows = torch.arange(0, t, 7, device="cuda")
+    want, off = ref.product(dy[rows].double(), w.double(), n)
+    ref.within(dx[rows].double(), want, off + ref.half_step(want, torch.float16), "dx")
+
+
 @pytest.mark.parametrize("tokens", [2, 70])
 def test_offsets_past_32_bits(tokens):
     """Weights of more than 4 GB."""

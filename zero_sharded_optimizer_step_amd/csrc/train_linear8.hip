@@ -176,6 +176,7 @@ struct Prepare {
     int64_t dyr_ld;
     int64_t share;            // rows of one share of the column sums
     int32_t column_blocks;    // of 256 columns
+    int32_t past;             // dy is more than the caches hold: read past them
     float* part;              // [shares][out], or
     unsigned short* db;       // the only share's sums in 16 bits
     uint32_t ends[4];         // the blocks' ranges end here
@@ -245,7 +246,8 @@ __device__ __forceinline__ void column_sums(const Prepare& q, uint32_t block) {
         }
     };
     typedef u32x4 eight __attribute__((aligned(2)));
-    if (q.out >= 8) add([&](const unsigned short* at) { return u32x4(*reinterpret_cast<const eight*>(at + d)); });
+    if (q.past) add([&](const unsigned short* at) { return u32x4(__builtin_nontemporal_load(reinterpret_cast<const eight*>(at + d))); });
+    else if (q.out >= 8) add([&](const unsigned short* at) { return u32x4(*reinterpret_cast<const eight*>(at + d)); });
     else add([&](const unsigned short* at) { return row_piece(at, d, q.out); });
     // columns of two threads have the same sums twice
     const int64_t from = d - static_cast<int64_t>(across) * 256;
@@ -508,6 +510,7 @@ constexpr int64_t kMaxTokens = int64_t(1) << 20, kMaxOut = int64_t(1) << 20;
 // and 16.1.  It loses at 64 x 16384 x 1024, 18.9 and 14.2: few rows, long ones.
 constexpr int64_t kFewTokens = 64, kMoreTokens = 1024, kFewParts = 512, kFewDim = 4096;
 constexpr int kTilesAtOnce = 2 * kCus;        // of 128 x 128
+constexpr int64_t kCacheBytes = int64_t(256) << 20;
 constexpr int64_t kMostPacks = 1 << 22;       // blocks; with the others' the grid's 32 bits hold them
 constexpr size_t kPieceBytes = size_t(512) << 20;
 
@@ -797,6 +800,9 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
         p.dyr_ld = dyr_ld;
         p.column_blocks = static_cast<int32_t>(up(n, 256) / 256);
         p.share = up(up(t, c.shares) / c.shares, 8);
+        // 8192 x 16384 98 us for 107 with w^ and x^; 2048 x 4096, which the
+        // products then find in the caches, 142 us in all for 140
+        p.past = n >= 8 && t * n * 2 >= kCacheBytes;
         p.part = part;
         p.db = c.shares == 1 ? static_cast<unsigned short*>(a->db) : nullptr;
         p.ends[0] = d == 0 && want_db ? static_cast<uint32_t>(p.column_blocks * c.shares) : 0;
