@@ -503,11 +503,11 @@ __global__ __launch_bounds__(256) void few_join_kernel(const FewJoin q) {
 constexpr int64_t kMaxTokens = int64_t(1) << 20, kMaxOut = int64_t(1) << 20;
 // few8_kernel's rule: up to 64 tokens; up to 1024 while its parts, 16 rows by
 // 64 tokens, are at most two rounds of the CUs and dim is short.  Microseconds,
-// and those of the tiles: 17 tokens x 4096 x 4096 6.9 and 15, x 16384 16.2 and
-// 24.5; 64 x 4096 x 16384 22.9 and 25.1, x 1000 x 10007 9.4 and 9.9; 128 x 4096
-// x 4096 (512 parts) 13.6 and 15.7, 512 x 512 x 512 4.6 and 6.4, but 192 x 4096
-// x 4096 (768) 28.5 and 22.7, 128 x 16384 x 4096 38 and 32, 8000 x 4096 x 64 28.5
-// and 16.1.  It loses at 64 x 16384 x 1024, 18.9 and 14.2: few rows, long ones.
+// and those of the tiles: 17 tokens x 4096 x 4096 6.9 and 11.6, x 16384 16 and
+// 24; 64 x 4096 x 16384 23.3 and 25.0, x 1000 x 10007 9.5 and 9.4; 128 x 4096 x
+// 4096 (512 parts) 13.6 and 15.0, 512 x 512 x 512 4.5 and 6.3, but 192 x 4096 x
+// 4096 (768) 28.5 and 17.1, 128 x 16384 x 4096 41 and 27, x 4096 x 16384 40 and
+// 25.  It loses at 64 x 16384 x 1024, 19 and 14: few rows, long ones.
 constexpr int64_t kFewTokens = 64, kMoreTokens = 1024, kFewParts = 512, kFewDim = 4096;
 constexpr int kTilesAtOnce = 2 * kCus;        // of 128 x 128
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
@@ -587,7 +587,7 @@ void few(const Few& q, hipStream_t st) {
 // at best, a slice's sums are written and read once each, and joining them is
 // a launch.  Microseconds with 1, 2, 3, 4 and 8 slices, and the rule's choice:
 // 256 tokens x 4096 x 4096 23.0, 20.1, 18.7, 18.5, 23.0 (3); 256 x 16384 x 4096
-// 67.5, 46.6, 37.4, 40.2, 39.6 (3); 512 x 4096 x 4096 23.5, 24.6, 26.6, 27.3,
+// 67.5, 46.6, 37.4 (46 elsewhere in memory), 40.2, 39.6 (3); 512 x 4096 x 4096 23.5, 24.6, 26.6, 27.3,
 // 43.9 (1); 700 x 8000 x 1500 43.3, 31.8, 26.4, 28.9, 32.8 (3).
 int forward_slices(int64_t tokens, int64_t dim, int64_t out) {
     const int64_t tiles = up(tokens, 128) / 128 * (up(out, 128) / 128), steps = up(dim, 128) / 128;
