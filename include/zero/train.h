@@ -340,7 +340,8 @@ typedef struct {
 int zero_glu8_forward(const zero_glu8_args* a, void* stream);
 
 /* Writes dgate and dup from dh, gate8 and up8 with their scales; gate, up, h
- * and h8 are not used.  dgate or dup may be dh itself, with its stride.
+ * and h8 are not used.  dgate or dup may be dh itself, with its stride; no other output
+ * may overlap an input or another output.
  * Errors as above. */
 int zero_glu8_backward(const zero_glu8_args* a, void* stream);
 

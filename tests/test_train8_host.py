@@ -77,6 +77,20 @@ def test_glu8_refuses_each_way(way, kw, code):
     assert call(ctypes.byref(glu_args(**kw)), None) == getattr(Z, "ZERO_" + code)
 
 
+@pytest.mark.parametrize("kw,why", [
+    (dict(), "dgate and dup"), (dict(dh=2 * A), "dgate and dup"),
+    (dict(dup=2 * A, dgate_stride=104), "another stride"), (dict(dgate=2 * A, dup_stride=104), "another stride"),
+    (dict(dup=2 * A, dh_stride=104), "another stride")])
+def test_glu8_gradients_in_one_memory(kw, why):
+    """dgate or dup may be dh's memory, with its stride, and neither the other's."""
+    call = train_lib().zero_glu8_backward
+    assert call(ctypes.byref(glu_args(**kw)), None) == Z.ZERO_EINVAL
+    assert why in Z.zero_last_error()
+    # where there is nothing to write it does not matter
+    for none in (dict(tokens=0), dict(width=0)):
+        assert call(ctypes.byref(glu_args(**{**kw, **none})), None) == Z.ZERO_OK
+
+
 def linear_args(**kw):
     a = zero_linear8_args()
     a.tokens, a.dim, a.out, a.dtype = 10, 100, 70, Z.ZERO_FP16

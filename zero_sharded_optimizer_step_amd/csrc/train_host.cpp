@@ -196,6 +196,12 @@ int check_glu8_args(const zero_glu8_args* a, bool backward) {
         if ((rc = check_rows("dh", a->dh, a->dh_stride, t, w, 2))) return rc;
         if ((rc = check_rows("dgate", a->dgate, a->dgate_stride, t, w, 2))) return rc;
         if (gated && (rc = check_rows("dup", a->dup, a->dup_stride, t, w, 2))) return rc;
+        if (t > 0 && w > 0) {
+            if (gated && a->dgate == a->dup) return fail(ZERO_EINVAL, "dgate and dup are the same memory");
+            if (t > 1 && ((a->dgate == a->dh && a->dgate_stride != a->dh_stride) ||
+                          (gated && a->dup == a->dh && a->dup_stride != a->dh_stride)))
+                return fail(ZERO_EINVAL, "a gradient in dh's memory has another stride");
+        }
         return ZERO_OK;
     }
     if ((rc = check_rows("gate", a->gate, a->gate_stride, t, w, 2))) return rc;
