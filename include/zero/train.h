@@ -354,7 +354,9 @@ int zero_glu8_backward(const zero_glu8_args* a, void* stream);
  *
  * x8: tokens rows of dim codes, w8: out rows of dim codes, each with its
  * rows' scales.  The forward's sums are whole numbers in 32 bits, exact; one
- * is scaled and the bias added in fp32 and rounded once.  The backward takes
+ * is multiplied in fp32 by x_scale, then by w_scale with the bias added, and
+ * rounded once (where its product with x_scale is past fp32's range, y is an
+ * infinity, however small w_scale).  The backward takes
  * x^ and w^ in dtype (exact where the scales are the encoder's for rows of
  * that dtype, else rounded to nearest even) times dy, with fp32 sums, and
  * rounds once.  Results do not depend on timing.

@@ -587,8 +587,9 @@ void few(const Few& q, hipStream_t st) {
 // at best, a slice's sums are written and read once each, and joining them is
 // a launch.  Microseconds with 1, 2, 3, 4 and 8 slices, and the rule's choice:
 // 256 tokens x 4096 x 4096 23.0, 20.1, 18.7, 18.5, 23.0 (3); 256 x 16384 x 4096
-// 67.5, 46.6, 37.4 (46 elsewhere in memory), 40.2, 39.6 (3); 512 x 4096 x 4096 23.5, 24.6, 26.6, 27.3,
-// 43.9 (1); 700 x 8000 x 1500 43.3, 31.8, 26.4, 28.9, 32.8 (3).
+// 67.5, 46.6, 37.4 (46 elsewhere in memory), 40.2, 39.6 (3); 512 x 4096 x 4096
+// 23.5, 24.6, 26.6, 27.3, 43.9 (1); 700 x 8000 x 1500 43.3, 31.8, 26.4, 28.9,
+// 32.8 (3).
 int forward_slices(int64_t tokens, int64_t dim, int64_t out) {
     const int64_t tiles = up(tokens, 128) / 128 * (up(out, 128) / 128), steps = up(dim, 128) / 128;
     const double operands = static_cast<double>(tiles) * 256.0 * static_cast<double>(dim) * 1e-7;
