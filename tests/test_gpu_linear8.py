@@ -114,6 +114,26 @@ def test_strides_and_alignment(pad, shift, code_pad):
         Call(*size, torch.float16, pad=pad, shift=shift, code_pad=code_pad).check()
 
 
+@pytest.mark.parametrize("size", [(3, 200, 104), (70, 520, 264), (300, 1000, 200), (2048, 1024, 2184)], ids=str)
+def test_what_lies_beside_dy_is_not_read(size):
+    """dy as columns of a wider matrix, aligned so that it is read where it
+    lies; a NaN there times the zeros past the last channel would show."""
+    t, k, n = size
+    say("linear8 beside dy %s" % (size,))
+    for dtype in DTYPES:
+        c = Call(t, k, n, dtype)
+        wide = torch.full((t + 8, n + 72), float("nan"), dtype=dtype, device="cuda")
+        wide[4:4 + t, 8:8 + n] = c.dy
+        Z.zero_linear8_backward(c.args)
+        want = c.dx.clone(), c.dw.clone(), c.db.clone()
+        for out in (c.dx, c.dw, c.db):
+            out.fill_(-7)
+        c.args.dy = wide[4:4 + t, 8:8 + n]
+        Z.zero_linear8_backward(c.args)
+        assert all(torch.equal(a, b) for a, b in zip((c.dx, c.dw, c.db), want))
+        c.clean()
+
+
 @pytest.mark.parametrize("size", [(3, 200, 100), (30, 2000, 100), (60, 80, 20), (300, 1000, 200)], ids=str)
 def test_any_codes_and_scales(size):
     """Codes down to -128 and scales that are no powers of two, which the gradient rounds once."""
