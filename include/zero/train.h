@@ -387,7 +387,8 @@ typedef struct {
  * all calls of these sizes that follow each other; no call reads what another
  * left there; calls that overlap, on two streams or in two graphs, need one
  * each).  It has room for a copy of dy, whose rows need not be whole 16-byte
- * pieces, and for at most 512 MB of x^ and w^ (of 256 columns, if more).
+ * pieces, and for at most 512 MB of x^ and w^ (of 256 columns, if more);
+ * of few tokens for parts of dx's sums alone.
  * 0 for out-of-range sizes.  Host only. */
 size_t zero_linear8_workspace_bytes(int64_t tokens, int64_t dim, int64_t out);
 

@@ -159,27 +159,22 @@ def test_sums_are_whole(tokens):
     c.check_forward()
 
 
-@pytest.mark.parametrize("size", [(1, 5, 3), (1, 513, 3000), (2, 1000, 4099), (2, 16, 70000), (3, 1027, 1100), (4, 3001, 400),
-                                  (5, 4100, 8200), (8, 600, 56000), (1, 131071, 65)], ids=str)
+@pytest.mark.parametrize("size", [(1, 5, 3), (1, 5, 8), (1, 513, 3000), (2, 1000, 4099), (2, 16, 70000), (3, 1027, 1100), (4, 3001, 400),
+                                  (5, 4100, 8200), (8, 600, 56000), (1, 131071, 65), (9, 30, 31), (16, 1000, 2053), (17, 129, 9),
+                                  (31, 2064, 777), (32, 128, 256), (33, 4096, 520), (48, 300, 9001), (49, 1030, 4100), (64, 127, 20011),
+                                  (64, 70000, 33), (64, 2048, 1024)], ids=str)
 def test_gradient_of_few_tokens(size):
-    """One pass over the weights.  A thread adds a quarter of a share's rows,
-    then four waves' and up to 512 shares' sums are joined 16 at once."""
+    """One pass over the weights.  A wave adds 32 rows of dx's sum at a time,
+    less than a 32nd of all of them, then eight waves' and up to 512 shares'
+    sums are joined, the latter 16 at once: 8 + 32 + 16 roundings, for which
+    the tiles' bound has 64.  A thread adds at most 8 pairs of db's sum, and
+    its 64 values meet in two more steps."""
     t, k, n = size
     say("linear8 few gradient %s" % (size,))
     for dtype, pad, shift in ((torch.bfloat16, 0, 0), (torch.float16, 3, 1)):
         c = Call(t, k, n, dtype, pad=pad, shift=shift, code_pad=16 * pad, any_codes=pad > 0)
         Z.zero_linear8_backward(c.args)
-        dy = c.dy.double()
-        w = c.sixteen_bits(c.w8, c.ws)
-        shares = max(1, min(512, 1024 // -(-(-(-k // 256) * 256) // 512), n // 32))
-        chain = -(-n // shares) / 4 + 1 + 4 + shares / 16 + 16
-        dx, off = dy @ w, chain * ref.U * (dy.abs() @ w.abs())
-        ref.within(c.dx.double(), dx, off + ref.half_step(dx, dtype), "dx")
-        x = c.sixteen_bits(c.x8, c.xs)
-        dw, off = dy.t() @ x, t * ref.U * (dy.abs().t() @ x.abs())
-        ref.within(c.dw.double(), dw, off + ref.half_step(dw, dtype), "dw")
-        db, off = dy.sum(0), t * ref.U * dy.abs().sum(0)
-        ref.within(c.db.double(), db, off + ref.half_step(db, dtype), "db")
+        c.check_backward()
         c.clean()
         # each alone gives the same
         for name in ("dx", "dw"):
@@ -306,7 +301,7 @@ def test_more_of_dy_than_the_caches_hold():
     ref.within(dx[rows].double(), want, off + ref.half_step(want, torch.float16), "dx")
 
 
-@pytest.mark.parametrize("tokens", [2, 70])
+@pytest.mark.parametrize("tokens", [2, 64, 70])
 def test_offsets_past_32_bits(tokens):
     """Weights of more than 4 GB."""
     dim, out = 4112, 1 << 20

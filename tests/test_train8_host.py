@@ -136,6 +136,8 @@ def test_linear8_workspace_sizes():
     size = Z.zero_linear8_workspace_bytes
     assert size(-1, 64, 64) == 0 and size(1, 131072, 64) == 0 and size(1, 64, (1 << 20) + 1) == 0
     assert size(0, 0, 0) > 0 and size(1, 1, 1) % 256 == 0
+    # few tokens: parts of dx's sums alone
+    assert size(1, 4096, 16384) <= 1 << 20 and size(64, 4096, 16384) <= 1 << 24
     # the largest: dy's rows made whole, and beside it not much more than what 256 columns of both operands take
     assert size(1 << 20, 131071, 1 << 20) < 2 * (1 << 40) + (1 << 31)
 

@@ -9,8 +9,9 @@
 //   backward   x^ and w^ are written out in 16 bits (exact with the encoder's
 //              scales), as many columns of dim at a time as 512 MB hold; then
 //              dx = dy w^ and dw = dy^T x^.  Small results are cut along
-//              their sum into slices, joined in a fixed order.  Up to 8
-//              tokens one pass over w8's rows makes dw's beside dx's sums.
+//              their sum into slices, joined in a fixed order.  Up to 64
+//              tokens one pass over w8's rows makes dw's beside dx's sums,
+//              with no copy in 16 bits.
 #include "train_product.h"
 
 namespace zero {
@@ -330,11 +331,19 @@ __global__ __launch_bounds__(256) void finish_kernel(const Finish q) {
     }
 }
 
-// The gradient of up to 8 tokens: w8 is read once and dw written once, and
-// nothing else counts.  A wave takes rows of both, a thread 8 columns of them;
-// x^ and dx's sums of those columns stay in its registers, 64 rows' dy and
-// scales lie in LDS.  A block's four waves join their sums there; the shares
-// of the rows, up to 512, are joined 16 at once by a second kernel.
+// The gradient of up to 64 tokens: w8 is read once and dw written once, and
+// little else counts.  A wave takes 32 rows of both at a time and 128 columns.
+// w^, whose sum runs over the rows, is turned in registers: a lane loads 8
+// columns of 8 rows, and what it has of a column is its part of a fragment.
+// dy goes to dx's products as it lies and to dw's turned by way of LDS, where
+// x^'s fragments lie too; a lane's dw are 8 columns of a row, one store.
+// Eight waves join their sums of dx in LDS, the shares of the rows by a
+// second kernel, or where there is one share that is dx.
+// Of 4096 x 16384 1 token takes 46 us (4.4 TB/s of w8 and dw), 16 49, 32 54 and
+// 64 63: 8 us more of products and conversions, 4 of joining.  Up to 16 tokens
+// two blocks share a CU (16 tokens: one 54).  Neighbouring columns' blocks run
+// on unlike XCDs; the other way round 1 token takes 52.  w8 read past the
+// caches: 47; dw written through them: 50.
 struct FewGradient {
     const char* w8;
     const char* x8;
@@ -342,123 +351,210 @@ struct FewGradient {
     const float *w_scale, *x_scale;
     const unsigned short* dy;
     int64_t dy_stride;
-    int64_t out, dim, share;  // rows of a share
-    int32_t tokens;
-    float* part;              // [shares][tokens][ld], or NULL: no dx
+    int32_t share;            // rows of a share, a multiple of 32
+    int32_t tokens, dim, out, want_dx;
+    float* part;              // [shares][tokens][ld], or NULL: one share
     int64_t ld;
+    unsigned short* dx;
+    int64_t dx_stride;
     unsigned short* dw;       // or NULL
     int64_t dw_stride;
     unsigned short* db;       // or NULL
 };
-constexpr int kFewColumns = 512;
+constexpr int kFewColumns = 128, kGradientWaves = 8, kFewRows = 32;
 
-// Eight held values as 16 bits hold them.
+// Column i of eight columns of codes of eight rows: a fragment.
 template <int DT>
-__device__ __forceinline__ void held8(const u32x2 c, float s, float o[8]) {
+__device__ __forceinline__ u32x4 turned8(const u32x2 (&c)[8], const float (&s)[8], int i) {
+    u32x4 o;
     #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const unsigned w = c[i / 2] >> (16 * (i % 2));
-        const unsigned h = pack2<DT>(static_cast<float>(static_cast<int8_t>(w)) * s,
-                                     static_cast<float>(static_cast<int8_t>(w >> 8)) * s);
-        o[2 * i] = lo_to_f32<DT>(h);
-        o[2 * i + 1] = hi_to_f32<DT>(h);
+    for (int r = 0; r < 4; ++r)
+        o[r] = pack2<DT>(static_cast<float>(static_cast<int8_t>(c[2 * r][i / 4] >> (8 * (i % 4)))) * s[2 * r],
+                         static_cast<float>(static_cast<int8_t>(c[2 * r + 1][i / 4] >> (8 * (i % 4)))) * s[2 * r + 1]);
+    return o;
+}
+
+template <int DT>
+__device__ __forceinline__ f32x4 product16(const u32x4 a, const u32x4 b, const f32x4 c) {
+    if constexpr (DT == ZERO_BF16) {
+        typedef __bf16 frag __attribute__((ext_vector_type(8)));
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
+    } else {
+        typedef _Float16 frag __attribute__((ext_vector_type(8)));
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(frag, a), __builtin_bit_cast(frag, b), c, 0, 0, 0);
     }
 }
 
-template <int DT, int T>
-__global__ __launch_bounds__(256) void few_gradient_kernel(const FewGradient q) {
-    constexpr int kRowsAtOnce = 64, kDeep = T > 4 ? 4 : 8; // rows of a block's turn; of a wave's whose loads go together
-    __shared__ float s_sum[4][kFewColumns];
-    __shared__ __attribute__((aligned(16))) float s_dy[kRowsAtOnce][T];
-    __shared__ float s_scale[kRowsAtOnce];
-    const int lane = threadIdx.x & 63;
+template <int DT, int NF>
+__global__ __launch_bounds__(kGradientWaves * 64, NF == 1 ? 4 : 2) void few_gradient_kernel(const FewGradient q) {
+    const int across = blockIdx.x, down = blockIdx.y;
+    constexpr int W = kGradientWaves, KH = NF > 2 ? 2 : 1, kTurned = 32 * KH + 8, kJoinRow = kFewColumns + 4;
+    constexpr int kHeldBytes = KH * 8 * 64 * 16, kLoopBytes = kHeldBytes + W * kFewRows * kTurned * 2;
+    constexpr int kJoinBytes = W * 16 * kJoinRow * 4;
+    __shared__ __attribute__((aligned(16))) char room[kLoopBytes > kJoinBytes ? kLoopBytes : kJoinBytes];
+    u32x4* const s_x = reinterpret_cast<u32x4*>(room);     // [half][column of a lane's 8][lane]
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int64_t d = static_cast<int64_t>(blockIdx.x) * kFewColumns + lane * 8;
-    const int64_t first = blockIdx.y * q.share, last = first + q.share < q.out ? first + q.share : q.out;
-    const bool in = d < q.dim;
-    const u32x2 none = {0u, 0u};
-    float x[T][8], sum[T][8];
-    #pragma unroll
-    for (int t = 0; t < T; ++t) {
+    unsigned short* const s_dy = reinterpret_cast<unsigned short*>(room + kHeldBytes) + wave * kFewRows * kTurned;
+    const int d = across * kFewColumns + c * 8;
+    const int first = down * q.share, last = first + q.share < q.out ? first + q.share : q.out;
+    u32x2 w[8];
+    f32x4 scale[2];
+    u32x4 dy[NF];
+    int past = 0;                                          // of dy's eight elements from the row's end on
+    // the wave's next 32 rows; past the last of them all are 0
+    auto load = [&](int row) __attribute__((always_inline)) -> void {
+        const int rows = row < last ? (q.out - row < kFewRows ? q.out - row : kFewRows) : 0, from = rows > 0 ? row : 0;
+        const __amdgpu_buffer_rsrc_t rw = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<char*>(q.w8 + from * q.w_row), 0, q.want_dx ? static_cast<int>(rows * q.w_row) : 0, 0x00020000);
+        const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<float*>(q.w_scale + from), 0, q.want_dx ? static_cast<int>(rows * 4) : 0, 0x00020000);
+        // offsets made here each time: kept from step to step they take registers that are not there
+        uint32_t o = g * 8 * static_cast<uint32_t>(q.w_row) + d;
+        asm volatile("" : "+v"(o));
         #pragma unroll
-        for (int e = 0; e < 8; ++e) x[t][e] = sum[t][e] = 0.0f;
-        if (q.dw && t < q.tokens)
-            held8<DT>(in ? *reinterpret_cast<const u32x2*>(q.x8 + t * q.x_row + d) : none, q.x_scale[t], x[t]);
+        for (int r = 0; r < 8; ++r)
+            w[r] = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                       rw, d < q.dim ? o + r * static_cast<uint32_t>(q.w_row) : kNowhere, 0, 0));
+        #pragma unroll
+        for (int r = 0; r < 2; ++r)
+            scale[r] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, g * 32 + r * 16, 0, 0));
+        // a row's end is taken out of its last eight elements
+        const int n = row + g * 8, at = n + 8 <= q.out ? n : q.out - 8;
+        past = n - at < 8 ? n - at : 8;
+        #pragma unroll
+        for (int j = 0; j < NF; ++j) {
+            typedef u32x4 eight __attribute__((aligned(2)));
+            const int t = j * 16 + c;
+            dy[j] = *reinterpret_cast<const eight*>(q.dy + (t < q.tokens ? t : q.tokens - 1) * q.dy_stride + at);
+        }
+    };
+    load(first + wave * kFewRows);
+    if (q.dw && wave < KH) {
+        u32x2 x[8];
+        float s[8];
+        #pragma unroll
+        for (int r = 0; r < 8; ++r) {
+            // codes of tokens past the last count nothing
+            const int t = wave * 32 + g * 8 + r, at = t < q.tokens ? t : q.tokens - 1;
+            x[r] = *reinterpret_cast<const u32x2*>(q.x8 + at * q.x_row + (d < q.dim ? d : 0));
+            s[r] = t < q.tokens ? q.x_scale[at] : 0.0f;
+        }
+        #pragma unroll
+        for (int i = 0; i < 8; ++i) s_x[(wave * 8 + i) * 64 + lane] = turned8<DT>(x, s, i);
     }
-    for (int64_t base = first; base < last; base += kRowsAtOnce) {
-        const int rows = last - base < kRowsAtOnce ? static_cast<int>(last - base) : kRowsAtOnce;
-        __syncthreads();
-        for (int i = threadIdx.x; i < kRowsAtOnce * T; i += 256) {
-            const int row = i % kRowsAtOnce, t = i / kRowsAtOnce;
-            s_dy[row][t] = row < rows && t < q.tokens ? lo_to_f32<DT>(q.dy[t * q.dy_stride + base + row]) : 0.0f;
-        }
-        if (q.part && static_cast<int>(threadIdx.x) < rows) s_scale[threadIdx.x] = q.w_scale[base + threadIdx.x];
-        __syncthreads();
-        if (q.db && blockIdx.x == 0 && static_cast<int>(threadIdx.x) < rows) {
-            float all = 0.0f;
+    __syncthreads();
+    f32x4 acc[8][NF] = {};
+    for (int row = first + wave * kFewRows; row < last; row += W * kFewRows) {
+        #pragma unroll
+        for (int j = 0; j < NF; ++j) dy[j] = past < 8 && j * 16 + c < q.tokens ? moved_down(dy[j], past) : u32x4{0u, 0u, 0u, 0u};
+        #pragma unroll
+        for (int j = 0; j < NF; ++j)
             #pragma unroll
-            for (int t = 0; t < T; ++t) all += s_dy[threadIdx.x][t];
-            q.db[base + threadIdx.x] = pack1<DT>(all);
-        }
-        for (int r = wave; r < rows; r += 4 * kDeep) {
-            u32x2 c[kDeep];
+            for (int e = 0; e < 8; ++e)
+                s_dy[(g * 8 + e) * kTurned + j * 16 + c] = static_cast<unsigned short>(dy[j][e / 2] >> (16 * (e % 2)));
+        if (q.want_dx) {
+            const float s[8] = {scale[0].x, scale[0].y, scale[0].z, scale[0].w, scale[1].x, scale[1].y, scale[1].z, scale[1].w};
             #pragma unroll
-            for (int i = 0; i < kDeep; ++i) {
-                const int64_t n = base + (r + 4 * i < rows ? r + 4 * i : r);
-                c[i] = q.part && in ? __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(q.w8 + n * q.w_row + d)) : none;
-            }
-            #pragma unroll
-            for (int i = 0; i < kDeep; ++i) {
-                const int row = r + 4 * i;
-                if (row >= rows) break;
-                // of tokens that there are not 0, as their x
-                float g[T];
+            for (int i = 0; i < 8; ++i) {
+                const u32x4 b = turned8<DT>(w, s, i);
                 #pragma unroll
-                for (int t = 0; t < T; ++t) g[t] = s_dy[row][t];
-                if (q.part) {
-                    float w[8];
-                    held8<DT>(c[i], s_scale[row], w);
+                for (int j = 0; j < NF; ++j) acc[i][j] = product16<DT>(dy[j], b, acc[i][j]);
+            }
+        }
+        load(row + W * kFewRows);
+        if (!q.dw && !(q.db && across == 0)) continue;
+        // the wave's own rows of LDS, written above by its other lanes
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        int64_t to0 = static_cast<int64_t>(row + g * 4) * q.dw_stride + d;
+        asm volatile("" : "+v"(to0));
+        #pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            u32x4 a[KH];
+            #pragma unroll
+            for (int h = 0; h < KH; ++h) {
+                a[h] = *reinterpret_cast<const u32x4*>(s_dy + (n * 16 + c) * kTurned + h * 32 + g * 8);
+                // nothing was written for the other half of the last product's sum
+                if (NF % 2 == 1 && h == KH - 1 && g >= 2) a[h] = u32x4{0u, 0u, 0u, 0u};
+            }
+            if (q.db && across == 0) {
+                float all = 0.0f;
+                #pragma unroll
+                for (int h = 0; h < KH; ++h)
                     #pragma unroll
-                    for (int t = 0; t < T; ++t) {
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e) sum[t][e] = __builtin_fmaf(g[t], w[e], sum[t][e]);
-                    }
-                }
-                if (q.dw && in) {
-                    float o[8] = {};
+                    for (int e = 0; e < 4; ++e) all += lo_to_f32<DT>(a[h][e]) + hi_to_f32<DT>(a[h][e]);
+                all += __shfl_xor(all, 16, 64);
+                all += __shfl_xor(all, 32, 64);
+                if (g == 0 && row + n * 16 + c < q.out) q.db[row + n * 16 + c] = pack1<DT>(all);
+            }
+            if (!q.dw) continue;
+            // two columns at a time: what waits for the others is in 16 bits
+            u32x4 v[4];
+            #pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                f32x4 o[2] = {};
+                #pragma unroll
+                for (int e = 0; e < 2; ++e)
                     #pragma unroll
-                    for (int t = 0; t < T; ++t) {
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e) o[e] = __builtin_fmaf(g[t], x[t][e], o[e]);
+                    for (int h = 0; h < KH; ++h) o[e] = product16<DT>(a[h], s_x[(h * 8 + i + e) * 64 + lane], o[e]);
+                #pragma unroll
+                for (int r = 0; r < 4; ++r) v[r][i / 2] = pack2<DT>(o[0][r], o[1][r]);
+            }
+            #pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (row + n * 16 + g * 4 + r >= q.out || d >= q.dim) continue;
+                typedef u32x4 eight __attribute__((aligned(2)));
+                typedef u32x2 four __attribute__((aligned(2)));
+                typedef uint32_t two __attribute__((aligned(2)));
+                unsigned short* to = q.dw + (to0 + (n * 16 + r) * q.dw_stride);
+                if (d + 8 <= q.dim) {
+                    __builtin_nontemporal_store(v[r], reinterpret_cast<eight*>(to));
+                } else {
+                    u32x4 x = v[r];
+                    const int left = q.dim - d;
+                    if (left & 4) {
+                        *reinterpret_cast<four*>(to) = u32x2{x.x, x.y};
+                        x.x = x.z;
+                        x.y = x.w;
+                        to += 4;
                     }
-                    const u32x4 v = {pack2<DT>(o[0], o[1]), pack2<DT>(o[2], o[3]), pack2<DT>(o[4], o[5]), pack2<DT>(o[6], o[7])};
-                    typedef u32x4 eight __attribute__((aligned(2)));
-                    unsigned short* to = q.dw + (base + row) * q.dw_stride + d;
-                    if (d + 8 <= q.dim) {
-                        __builtin_nontemporal_store(v, reinterpret_cast<eight*>(to));
-                    } else {
-                        #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (d + e < q.dim) to[e] = static_cast<unsigned short>(v[e / 2] >> (16 * (e % 2)));
+                    if (left & 2) {
+                        *reinterpret_cast<two*>(to) = x.x;
+                        x.x = x.y;
+                        to += 2;
                     }
+                    if (left & 1) *to = static_cast<unsigned short>(x.x);
                 }
             }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
     }
-    if (!q.part) return;
-    float* part = q.part + static_cast<int64_t>(blockIdx.y) * q.tokens * q.ld;
+    if (!q.want_dx) return;
+    float* const s_join = reinterpret_cast<float*>(room);  // [wave][16 tokens][kJoinRow]
     #pragma unroll
-    for (int t = 0; t < T; ++t) {
-        if (t >= q.tokens) break;
+    for (int j = 0; j < NF; ++j) {
         __syncthreads();
         #pragma unroll
-        for (int e = 0; e < 8; ++e) s_sum[wave][lane * 8 + e] = sum[t][e];
+        for (int r = 0; r < 4; ++r)
+            #pragma unroll
+            for (int i = 0; i < 8; i += 4)
+                *reinterpret_cast<f32x4*>(s_join + (wave * 16 + g * 4 + r) * kJoinRow + c * 8 + i) =
+                    f32x4{acc[i][j][r], acc[i + 1][j][r], acc[i + 2][j][r], acc[i + 3][j][r]};
         __syncthreads();
+        const int in = threadIdx.x / 32, at = threadIdx.x % 32 * 4, t = j * 16 + in, column = across * kFewColumns + at;
+        f32x4 x = *reinterpret_cast<const f32x4*>(s_join + in * kJoinRow + at);
         #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int at = e * 256 + threadIdx.x;
-            const int64_t column = static_cast<int64_t>(blockIdx.x) * kFewColumns + at;
-            if (column < q.ld) part[t * q.ld + column] = (s_sum[0][at] + s_sum[1][at]) + (s_sum[2][at] + s_sum[3][at]);
+        for (int v = 1; v < W; ++v) x += *reinterpret_cast<const f32x4*>(s_join + (v * 16 + in) * kJoinRow + at);
+        if (t >= q.tokens) continue;
+        if (q.part) {
+            if (column < q.ld)
+                *reinterpret_cast<f32x4*>(q.part + (static_cast<int64_t>(down) * q.tokens + t) * q.ld + column) = x;
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (column + e < q.dim) q.dx[t * q.dx_stride + column + e] = pack1<DT>(x[e]);
         }
     }
 }
@@ -524,13 +620,19 @@ struct Cut {
     size_t total;
 };
 
-// Whether few_gradient_kernel takes it.  Microseconds, and those of the tiles:
-// 1 token x 4096 x 16384 46 and 114, x 4096 15 and 36, x 64 x 64 7.3 and 7.9;
-// 4 tokens x 1000 x 2053 13 and 16, x 200 x 300 10.9 and 9.6; 8 tokens x 4096 x
-// 16384 95 and 114, x 512 x 100000 73 and 93, x 4096 x 4096 38 and 36.
+// Whether few_gradient_kernel takes it: up to 32 tokens, and up to 64 of weights
+// that are not small, where the tiles' three launches are the shorter chain.
+// Microseconds, and those of the tiles: 64 tokens x 4096 x 16384 63 and 125, x
+// 1024 x 16384 26 and 44, x 1000 x 4100 16.8 and 18.7, x 2048 x 1000 15.6 and
+// 16.8, but x 1000 x 2053 18.7 and 16.5, x 200 x 300 12.7 and 9.5; 32 tokens x
+// 1000 x 2053 14.1 and 15.8, x 200 x 300 9.3 and 9.2; 16 x 200 x 300 8.1 and
+// 9.2, x 64 x 64 5.9 and 7.3; 1 x 1000 x 4100 11.6, where a kernel without
+// matrix cores took 10.6, but x 64 x 64 5.7 and 7.0.
+constexpr int64_t kFewGradientTokens = 32, kMoreGradientTokens = 64, kMoreWeights = int64_t(1) << 21;
 bool few_gradient_rule(int64_t tokens, int64_t dim, int64_t out) {
-    const int64_t weights = dim * out;
-    return tokens <= 2 || (tokens <= 4 && weights >= int64_t(1) << 20) || (tokens <= 8 && weights >= int64_t(1) << 25);
+    // a row of dy has whole pieces to take its end out of
+    if (out < 8) return false;
+    return tokens <= kFewGradientTokens || (tokens <= kMoreGradientTokens && dim * out >= kMoreWeights);
 }
 
 bool cut(int64_t tokens, int64_t dim, int64_t out, Cut* c) {
@@ -559,12 +661,15 @@ bool cut(int64_t tokens, int64_t dim, int64_t out, Cut* c) {
     c->dw_slab = c->dw_slices > 1 ? round_up(static_cast<size_t>(c->dw_slices) * n * c->piece * 4, 256) : 0;
     c->part_bytes = round_up(static_cast<size_t>(c->shares) * n * 4, 256);
     c->total = c->x_bytes + c->w_bytes + c->dy_bytes + c->dx_slab + c->dw_slab + c->part_bytes;
-    int64_t few = 1024 / (up(k, kFewColumns) / kFewColumns);
-    if (few > n / 32) few = n / 32;
-    c->few_shares = static_cast<int32_t>(few < 1 ? 1 : (few > 512 ? 512 : few));
+    // one or two blocks a CU, a step or more for each of their waves
+    int64_t few = kCus * (t <= 16 ? 2 : 1) / (up(k, kFewColumns) / kFewColumns);
+    if (few > n / (kGradientWaves * kFewRows)) few = n / (kGradientWaves * kFewRows);
+    c->few_shares = static_cast<int32_t>(few < 1 ? 1 : few);
     if (few_gradient_rule(t, dim, n)) {
+        // nothing is written out in 16 bits; db alone may still be asked for
+        c->x_bytes = c->w_bytes = c->dy_bytes = c->dx_slab = c->dw_slab = 0;
         const size_t sums = round_up(static_cast<size_t>(c->few_shares) * t * up(k, 8) * 4, 256);
-        if (c->total < sums) c->total = sums;
+        c->total = c->part_bytes > sums ? c->part_bytes : sums;
     }
     return true;
 }
@@ -745,23 +850,25 @@ int few_gradient(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
     q.x_scale = a->x_scale;
     q.dy = static_cast<const unsigned short*>(a->dy);
     q.dy_stride = a->dy_stride;
-    q.out = a->out;
-    q.dim = a->dim;
-    q.share = up(up(a->out, c.few_shares) / c.few_shares, 4);
+    q.out = static_cast<int32_t>(a->out);
+    q.dim = static_cast<int32_t>(a->dim);
+    q.share = static_cast<int32_t>(up(up(a->out, c.few_shares) / c.few_shares, kFewRows));
     q.tokens = static_cast<int32_t>(a->tokens);
-    q.part = a->dx ? static_cast<float*>(a->workspace) : nullptr;
+    q.want_dx = a->dx != nullptr;
+    q.part = a->dx && c.few_shares > 1 ? static_cast<float*>(a->workspace) : nullptr;
     q.ld = up(a->dim, 8);
+    q.dx = static_cast<unsigned short*>(a->dx);
+    q.dx_stride = a->dx_stride;
     q.dw = static_cast<unsigned short*>(a->dw);
     q.dw_stride = a->dw_stride;
     q.db = static_cast<unsigned short*>(a->db);
     const dim3 grid(static_cast<unsigned>(up(a->dim, kFewColumns) / kFewColumns), static_cast<unsigned>(c.few_shares));
-    if (a->tokens <= 1) hipLaunchKernelGGL((few_gradient_kernel<DT, 1>), grid, dim3(256), 0, st, q);
-    else if (a->tokens <= 2) hipLaunchKernelGGL((few_gradient_kernel<DT, 2>), grid, dim3(256), 0, st, q);
-    else if (a->tokens <= 4) hipLaunchKernelGGL((few_gradient_kernel<DT, 4>), grid, dim3(256), 0, st, q);
-    else hipLaunchKernelGGL((few_gradient_kernel<DT, 8>), grid, dim3(256), 0, st, q);
-    if (a->dx) {
-        const FewJoin j = {q.part, q.ld, c.few_shares, q.tokens, static_cast<int32_t>(a->dim),
-                           static_cast<unsigned short*>(a->dx), a->dx_stride};
+    if (a->tokens <= 16) hipLaunchKernelGGL((few_gradient_kernel<DT, 1>), grid, dim3(kGradientWaves * 64), 0, st, q);
+    else if (a->tokens <= 32) hipLaunchKernelGGL((few_gradient_kernel<DT, 2>), grid, dim3(kGradientWaves * 64), 0, st, q);
+    else if (a->tokens <= 48) hipLaunchKernelGGL((few_gradient_kernel<DT, 3>), grid, dim3(kGradientWaves * 64), 0, st, q);
+    else hipLaunchKernelGGL((few_gradient_kernel<DT, 4>), grid, dim3(kGradientWaves * 64), 0, st, q);
+    if (q.part) {
+        const FewJoin j = {q.part, q.ld, c.few_shares, q.tokens, q.dim, q.dx, q.dx_stride};
         hipLaunchKernelGGL((few_join_kernel<DT>), dim3(static_cast<unsigned>((a->tokens * (q.ld / 4) + 15) / 16)), dim3(256), 0,
                            st, j);
     }
@@ -770,7 +877,7 @@ int few_gradient(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
 
 template <int DT>
 int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
-    if (a->tokens > 0 && a->dim > 0 && few_gradient_rule(a->tokens, a->dim, a->out) && (a->dx || (a->dw && a->out > 0)))
+    if (a->tokens > 0 && a->dim > 0 && (a->dx || a->dw) && few_gradient_rule(a->tokens, a->dim, a->out))
         return few_gradient<DT>(a, c, st);
     char* ws = static_cast<char*>(a->workspace);
     unsigned short* x16 = reinterpret_cast<unsigned short*>(ws);
