@@ -188,6 +188,19 @@ def test_gradient_of_few_tokens(size):
                 setattr(c.args, other, getattr(c, other))
 
 
+@pytest.mark.parametrize("size", [(1, 40, 5), (5, 40, 30), (20, 300, 2001), (64, 2048, 1100), (130, 20, 300)], ids=str)
+def test_column_sums_alone(size):
+    """db alone, in the workspace that few tokens need little of."""
+    say("linear8 db alone %s" % (size,))
+    c = Call(*size, torch.float16, pad=1)
+    c.args.dx = c.args.dw = c.args.x8 = c.args.x_scale = c.args.w8 = c.args.w_scale = None
+    Z.zero_linear8_backward(c.args)
+    db, off = ref.column_sum(c.dy, c.t)
+    ref.within(c.db.double(), db, off + ref.half_step(db, torch.float16), "db")
+    assert bool((c.dx == -7).all()) and bool((c.dw == -7).all())
+    c.clean()
+
+
 @pytest.mark.parametrize("size", [(20, 90, 40), (200, 700, 300)], ids=str)
 def test_tokens_and_channels_that_are_not_finite(size):
     """A NaN scale is one token's or one channel's in y, that channel's share of every dx and that token's of every dw."""
