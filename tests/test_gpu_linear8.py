@@ -98,7 +98,8 @@ def test_large_tiles(size):
     Call(*size, torch.bfloat16, bias=False).check()
 
 
-@pytest.mark.parametrize("size", [(700, 3000, 1501), (130, 5000, 3001), (1500, 4200, 260), (260, 16400, 515), (1100, 2100, 130)],
+@pytest.mark.parametrize("size", [(700, 3000, 1501), (130, 5000, 3001), (1500, 4200, 260), (260, 16400, 515), (1100, 2100, 130),
+                                  (1, 16400, 1024), (17, 12300, 1001), (50, 9000, 2048), (64, 40000, 70), (3, 100001, 9)],
                          ids=str)
 def test_sums_cut_into_slices(size):
     """So few tiles and so long a sum that the forward's is cut too, with odd rows of the parts."""
@@ -142,12 +143,13 @@ def test_any_codes_and_scales(size):
         Call(*size, dtype, any_codes=True).check()
 
 
+@pytest.mark.parametrize("out", [20, 1040])
 @pytest.mark.parametrize("tokens", [1, 20, 200])
-def test_sums_are_whole(tokens):
+def test_sums_are_whole(tokens, out):
     """The longest row of the largest codes: past 2^24 no fp32 sum would be exact."""
     dim = 131071
-    say("linear8 longest %d" % tokens)
-    c = Call(tokens, dim, 20, torch.float16, bias=False)
+    say("linear8 longest %d x %d" % (tokens, out))
+    c = Call(tokens, dim, out, torch.float16, bias=False)
     for codes, scale in ((c.x8, c.xs), (c.w8, c.ws)):
         codes[:, :dim] = -128
         scale.fill_(2.0**-13)

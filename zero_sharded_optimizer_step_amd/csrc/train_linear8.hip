@@ -603,7 +603,12 @@ constexpr int64_t kMaxTokens = int64_t(1) << 20, kMaxOut = int64_t(1) << 20;
 // 24; 64 x 4096 x 16384 23.3 and 25.0, x 1000 x 10007 9.5 and 9.4; 128 x 4096 x
 // 4096 (512 parts) 13.6 and 15.0, 512 x 512 x 512 4.5 and 6.3, but 192 x 4096 x
 // 4096 (768) 28.5 and 17.1, 128 x 16384 x 4096 41 and 27, x 4096 x 16384 40 and
-// 25.  It loses at 64 x 16384 x 1024, 19 and 14: few rows, long ones.
+// 25.  Few rows that are long leave its blocks one after another's loads, 0.3 to
+// 0.5 us for 512 of k, and CUs idle that slices of tiles would use: 64 x 16384 x
+// 1024 18.8 and 14.1, x 300 17.8 and 11.8, 17 x 16384 x 1024 13.6 and 12.7, 1 x
+// 65536 x 128 33 and 16, x 32768 x 900 18.6 and 15.3, but 64 x 8192 x 1024 12.0
+// and 12.0, 17 x 10000 x 512 9.9 and 11.3, 1 x 16384 x 1024 11.2 and 12.0, 32 x
+// 16384 x 2048 14.2 and 15.4.
 constexpr int64_t kFewTokens = 64, kMoreTokens = 1024, kFewParts = 512, kFewDim = 4096;
 constexpr int kTilesAtOnce = 2 * kCus;        // of 128 x 128
 constexpr int64_t kCacheBytes = int64_t(256) << 20;
@@ -712,7 +717,8 @@ int forward_slices(int64_t tokens, int64_t dim, int64_t out) {
     return best;
 }
 bool few_rows(int64_t tokens, int64_t dim, int64_t out) {
-    if (tokens <= kFewTokens) return true;
+    const bool thin = out <= (tokens > 32 ? 2048 : 1024) && dim > (tokens > 32 ? 8192 : (tokens > 16 ? 12288 : 16384));
+    if (tokens <= kFewTokens) return !thin;
     return tokens <= kMoreTokens && dim <= kFewDim && (out + 15) / 16 * ((tokens + 63) / 64) <= kFewParts;
 }
 
