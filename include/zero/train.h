@@ -299,6 +299,7 @@ int zero_rows8_decode(const void* codes, int64_t codes_stride, const float* scal
  *   ZERO_GLU_SILU  act(x) = x p, p = 1 / (1 + exp(-x))
  *   ZERO_GLU_GELU  act(x) = x p, p = 1 / (1 + exp(-2 sqrt(2/pi) (x + 0.044715 x^3)))
  *                  (the tanh form of gelu: p = (1 + tanh(..)) / 2)
+ *   p is held in fp32, below 2^-126 to the nearest multiple of 2^-149.
  *
  * Results depend on the inputs alone.  A token whose gate or up holds an
  * infinity or a NaN has NaN in all of the gradients that read that row of
