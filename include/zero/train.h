@@ -384,19 +384,35 @@ typedef struct {
     size_t workspace_bytes;
 } zero_linear8_args;
 
-/* Bytes of workspace forward and backward need (one buffer serves both and
- * all calls of these sizes that follow each other; no call reads what another
- * left there; calls that overlap, on two streams or in two graphs, need one
- * each).  It has room for a copy of dy, whose rows need not be whole 16-byte
- * pieces, and for at most 512 MB of x^ and w^ (of 256 columns, if more);
- * of few tokens for parts of dx's sums alone.
- * 0 for out-of-range sizes.  Host only. */
+/* Bytes of workspace that calls of up to `tokens` tokens need: of the forward
+ * (ZERO_LINEAR8_FORWARD), of a backward whose dy is read where it lies
+ * (ZERO_LINEAR8_BACKWARD: dy 16-byte aligned, out and dy_stride multiples of
+ * 8, dy_stride at most 2^21) and of one whose dy may lie anyhow
+ * (ZERO_LINEAR8_BACKWARD_ANY_DY); the largest of the uses named.  One buffer
+ * serves them all and all calls that follow each other; no call reads what
+ * another left there; calls that overlap, on two streams or in two graphs,
+ * need one each.  It never falls as tokens rise.
+ * The forward uses it for the whole sums of slices of dim, where few tiles and
+ * a long dim are cut so (34 MB at most, mostly nothing: 256 bytes).  The
+ * backward has in it at most 512 MB of x^ and w^ in 16 bits (of 256 columns,
+ * if that is more), fp32 parts of dx and dw where their sums are cut (34 MB
+ * each), shares of db's sum, and a copy of dy, 2 tokens out bytes, where its
+ * rows are not read as they lie.  Of few tokens it has parts of dx's sums or
+ * shares of db's alone.
+ * 0 for out-of-range sizes or uses.  Host only; a search over the numbers of
+ * tokens, 10 us to 1 ms. */
+#define ZERO_LINEAR8_FORWARD 1
+#define ZERO_LINEAR8_BACKWARD 2
+#define ZERO_LINEAR8_BACKWARD_ANY_DY 4
+size_t zero_linear8_workspace_bytes_for(int64_t tokens, int64_t dim, int64_t out, int32_t uses);
+
+/* That of the forward and any backward. */
 size_t zero_linear8_workspace_bytes(int64_t tokens, int64_t dim, int64_t out);
 
 /* Writes y; dy, dx, dw and db are not used.  No output may overlap an input.
  * Errors: NULL or out-of-range arguments -> ZERO_EINVAL; misalignment ->
- * ZERO_EALIGN; workspace_bytes too small -> ZERO_ESIZE; launch ->
- * ZERO_EDEVICE. */
+ * ZERO_EALIGN; workspace_bytes less than this call uses -> ZERO_ESIZE; launch
+ * -> ZERO_EDEVICE. */
 int zero_linear8_forward(const zero_linear8_args* a, void* stream);
 
 /* Writes those of dx, dw and db that are given from dy, w8 (dx) and x8 (dw)

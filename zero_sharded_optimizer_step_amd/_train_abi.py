@@ -15,6 +15,7 @@ ZERO_STATE8_BLOCK = 256
 ZERO_MAX_GROUPS = 8
 ZERO_ROWS8_MAX_DIM = 131071
 ZERO_GLU_SILU, ZERO_GLU_GELU = 0, 1
+ZERO_LINEAR8_FORWARD, ZERO_LINEAR8_BACKWARD, ZERO_LINEAR8_BACKWARD_ANY_DY = 1, 2, 4
 u32, u64 = ctypes.c_uint32, ctypes.c_uint64
 
 
@@ -106,6 +107,7 @@ _PROTOTYPES = {
     "zero_glu8_forward": (ctypes.c_int, [_P(zero_glu8_args), vp]),
     "zero_glu8_backward": (ctypes.c_int, [_P(zero_glu8_args), vp]),
     "zero_linear8_workspace_bytes": (sz, [i64, i64, i64]),
+    "zero_linear8_workspace_bytes_for": (sz, [i64, i64, i64, i32]),
     "zero_linear8_forward": (ctypes.c_int, [_P(zero_linear8_args), vp]),
     "zero_linear8_backward": (ctypes.c_int, [_P(zero_linear8_args), vp]),
 }

@@ -215,7 +215,7 @@ int check_glu8_args(const zero_glu8_args* a, bool backward) {
 int check_linear8_args(const zero_linear8_args* a, bool backward) {
     if (!a) return fail(ZERO_EINVAL, "args is NULL");
     if (a->tokens < 0 || a->dim < 0 || a->out < 0) return fail(ZERO_EINVAL, "a size is negative");
-    const size_t need = zero_linear8_workspace_bytes(a->tokens, a->dim, a->out);
+    const size_t need = linear8_needs(a, backward);
     if (!need)
         return fail(ZERO_EINVAL, "tokens %lld, dim %lld, out %lld are out of range", (long long)a->tokens,
                     (long long)a->dim, (long long)a->out);

@@ -46,5 +46,7 @@ int check_rows8(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, in
                 int64_t codes_stride, const float* scale);
 int check_glu8_args(const zero_glu8_args* a, bool backward);
 int check_linear8_args(const zero_linear8_args* a, bool backward);
+// Bytes of workspace that this call uses; 0 for out-of-range sizes.
+size_t linear8_needs(const zero_linear8_args* a, bool backward);
 
 }  // namespace zero

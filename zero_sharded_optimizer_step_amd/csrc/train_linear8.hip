@@ -615,7 +615,8 @@ constexpr int64_t kCacheBytes = int64_t(256) << 20;
 constexpr int64_t kMostPacks = 1 << 22;       // blocks; with the others' the grid's 32 bits hold them
 constexpr size_t kPieceBytes = size_t(512) << 20;
 
-// How a gradient is cut: by the three sizes alone.
+// How a gradient is cut: by the three sizes alone.  Its workspace has a copy of
+// dy's rows besides, where they are not read as they lie.
 struct Cut {
     int64_t piece;            // columns of dim at a time, a multiple of 256
     int32_t dx_slices, dw_slices;
@@ -640,9 +641,12 @@ bool few_gradient_rule(int64_t tokens, int64_t dim, int64_t out) {
     return tokens <= kFewGradientTokens || (tokens <= kMoreGradientTokens && dim * out >= kMoreWeights);
 }
 
-bool cut(int64_t tokens, int64_t dim, int64_t out, Cut* c) {
-    if (tokens < 0 || tokens > kMaxTokens || dim < 0 || dim > ZERO_ROWS8_MAX_DIM || out < 0 || out > kMaxOut)
-        return false;
+bool in_range(int64_t tokens, int64_t dim, int64_t out) {
+    return tokens >= 0 && tokens <= kMaxTokens && dim >= 0 && dim <= ZERO_ROWS8_MAX_DIM && out >= 0 && out <= kMaxOut;
+}
+
+bool cut(int64_t tokens, int64_t dim, int64_t out, bool copy_dy, Cut* c) {
+    if (!in_range(tokens, dim, out)) return false;
     const int64_t t = tokens > 0 ? tokens : 1, k = up(dim > 0 ? dim : 1, 256), n = out > 0 ? out : 1;
     int64_t piece = static_cast<int64_t>(kPieceBytes / (2 * static_cast<size_t>(t + n))) / 256 * 256;
     c->piece = piece < 256 ? 256 : (piece > k ? k : piece);
@@ -661,7 +665,7 @@ bool cut(int64_t tokens, int64_t dim, int64_t out, Cut* c) {
     c->shares = static_cast<int32_t>(shares < 1 ? 1 : shares);
     c->x_bytes = round_up(static_cast<size_t>(t * c->piece) * 2, 256);
     c->w_bytes = round_up(static_cast<size_t>(n * c->piece) * 2, 256);
-    c->dy_bytes = round_up(static_cast<size_t>(t * up(n, 64)) * 2, 256);
+    c->dy_bytes = copy_dy ? round_up(static_cast<size_t>(t * up(n, 64)) * 2, 256) : 0;
     c->dx_slab = c->dx_slices > 1 ? round_up(static_cast<size_t>(c->dx_slices) * t * c->piece * 4, 256) : 0;
     c->dw_slab = c->dw_slices > 1 ? round_up(static_cast<size_t>(c->dw_slices) * n * c->piece * 4, 256) : 0;
     c->part_bytes = round_up(static_cast<size_t>(c->shares) * n * 4, 256);
@@ -756,6 +760,58 @@ __global__ __launch_bounds__(256) void join_kernel(const Join q) {
         for (int e = 0; e < 4; ++e)
             if (m + e < q.out) o[e] = pack1<OT>(x[e]);
     }
+}
+
+// Bytes of workspace that a call uses, 256 at least.
+constexpr size_t kLeastBytes = 256;
+size_t forward_bytes(int64_t tokens, int64_t dim, int64_t out) {
+    const int slices = few_rows(tokens, dim, out) ? 1 : forward_slices(tokens, dim, out);
+    const size_t sums = slices > 1 ? static_cast<size_t>(slices) * tokens * up(out, 64) * 4 : 0;
+    return sums > kLeastBytes ? round_up(sums, 256) : kLeastBytes;
+}
+size_t backward_bytes(int64_t tokens, int64_t dim, int64_t out, bool copy_dy) {
+    Cut c;
+    if (!cut(tokens, dim, out, copy_dy, &c)) return 0;
+    return c.total > kLeastBytes ? c.total : kLeastBytes;
+}
+
+// And the most that calls of up to so many tokens use: fewer tokens may be cut
+// into more slices, or have wider pieces of columns.
+size_t most_forward_bytes(int64_t tokens, int64_t dim, int64_t out) {
+    size_t most = kLeastBytes;
+    // none with more tiles than half of the chip's is cut
+    for (int64_t t = 1; t <= tokens && 2 * (up(t, 128) / 128) * (up(out, 128) / 128) <= kTilesAtOnce; ++t) {
+        const size_t b = forward_bytes(t, dim, out);
+        most = b > most ? b : most;
+    }
+    return most;
+}
+size_t most_backward_bytes(int64_t tokens, int64_t dim, int64_t out, bool copy_dy) {
+    size_t most = backward_bytes(tokens, dim, out, copy_dy);
+    // Between two of these nothing but the tokens grows: rules end at 16, 32 and
+    // 64, tiles and shares change at multiples of 64 or behind them, and a
+    // narrower piece begins where its width no longer divides kPieceBytes so.
+    auto look = [&](int64_t t) {
+        if (t < 1 || t >= tokens) return;
+        const size_t b = backward_bytes(t, dim, out, copy_dy);
+        most = b > most ? b : most;
+    };
+    look(16);
+    look(32);
+    for (int64_t t = 64; t <= tokens; t += 64) {
+        look(t - 1);
+        look(t);
+    }
+    const int64_t n = out > 0 ? out : 1;
+    for (int64_t wide = 256; wide <= up(dim, 256); wide += 256)
+        look(static_cast<int64_t>(kPieceBytes) / 2 / wide - n);
+    return most;
+}
+
+// Whether the products need a copy of dy's rows.
+bool copies_dy(const zero_linear8_args* a) {
+    const bool any = a->dim > 0 && ((a->dx && a->tokens > 0) || (a->dw && a->out > 0));
+    return any && a->tokens > 0 && a->out > 0 && !whole_pieces(a->dy, a->dy_stride, a->out);
 }
 
 template <int OT>
@@ -894,7 +950,7 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
     float* part = dw_slab + c.dw_slab / 4;
     const int64_t t = a->tokens, n = a->out;
     const bool want_dx = a->dx && t > 0 && a->dim > 0, want_dw = a->dw && n > 0 && a->dim > 0, want_db = a->db && n > 0;
-    const bool whole = whole_pieces(a->dy, a->dy_stride, n), repack = !whole && t > 0 && n > 0 && (want_dx || want_dw);
+    const bool repack = copies_dy(a);
     const int64_t dyr_ld = up(n, 64);
     const int64_t last = want_dx || want_dw ? a->dim : 1;   // db alone: once
     for (int64_t d = 0; d < last; d += c.piece) {
@@ -933,8 +989,8 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
             q->lda = c.piece * 2;
             q->m = static_cast<int32_t>(up(wide, 8));
             // no row or no column: nothing of dy is read
-            q->b = whole ? static_cast<const char*>(a->dy) : reinterpret_cast<const char*>(dyr);
-            q->ldb = (whole ? a->dy_stride : dyr_ld) * 2;
+            q->b = repack ? reinterpret_cast<const char*>(dyr) : static_cast<const char*>(a->dy);
+            q->ldb = (repack ? dyr_ld : a->dy_stride) * 2;
         };
         if (want_dx) {
             unsigned short* out = static_cast<unsigned short*>(a->dx) + d;
@@ -973,18 +1029,31 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
 }
 
 }  // namespace
+
+size_t linear8_needs(const zero_linear8_args* a, bool backward) {
+    if (!in_range(a->tokens, a->dim, a->out)) return 0;
+    return backward ? backward_bytes(a->tokens, a->dim, a->out, copies_dy(a)) : forward_bytes(a->tokens, a->dim, a->out);
+}
+
 }  // namespace zero
 
 using namespace zero;
 
 extern "C" {
 
+size_t zero_linear8_workspace_bytes_for(int64_t tokens, int64_t dim, int64_t out, int32_t uses) {
+    constexpr int32_t kAll = ZERO_LINEAR8_FORWARD | ZERO_LINEAR8_BACKWARD | ZERO_LINEAR8_BACKWARD_ANY_DY;
+    if (!in_range(tokens, dim, out) || uses <= 0 || (uses & ~kAll)) return 0;
+    size_t most = kLeastBytes;
+    auto with = [&](size_t b) { most = b > most ? b : most; };
+    if (uses & ZERO_LINEAR8_FORWARD) with(most_forward_bytes(tokens, dim, out));
+    if (uses & ZERO_LINEAR8_BACKWARD) with(most_backward_bytes(tokens, dim, out, false));
+    if (uses & ZERO_LINEAR8_BACKWARD_ANY_DY) with(most_backward_bytes(tokens, dim, out, true));
+    return most;
+}
+
 size_t zero_linear8_workspace_bytes(int64_t tokens, int64_t dim, int64_t out) {
-    Cut c;
-    if (!cut(tokens, dim, out, &c)) return 0;
-    const int slices = few_rows(tokens, dim, out) ? 1 : forward_slices(tokens, dim, out);
-    const size_t sums = slices > 1 ? static_cast<size_t>(slices) * tokens * up(out, 64) * 4 : 0;
-    return c.total > sums ? c.total : round_up(sums, 256);
+    return zero_linear8_workspace_bytes_for(tokens, dim, out, ZERO_LINEAR8_FORWARD | ZERO_LINEAR8_BACKWARD_ANY_DY);
 }
 
 int zero_linear8_forward(const zero_linear8_args* a, void* stream) {
@@ -1000,7 +1069,7 @@ int zero_linear8_backward(const zero_linear8_args* a, void* stream) {
     const int rc = check_linear8_args(a, true);
     if (rc || (a->tokens == 0 && a->out == 0)) return rc;
     Cut c;
-    cut(a->tokens, a->dim, a->out, &c);
+    cut(a->tokens, a->dim, a->out, copies_dy(a), &c);
     hipStream_t st = static_cast<hipStream_t>(stream);
     return a->dtype == ZERO_BF16 ? backward<ZERO_BF16>(a, c, st) : backward<ZERO_FP16>(a, c, st);
 }

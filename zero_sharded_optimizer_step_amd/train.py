@@ -17,10 +17,10 @@ from typing import Optional, Sequence
 # imported at the end of the package's own module, which defines these
 from . import _dptr, _need, _stream, _torch, dtype_code
 from ._abi import check, lib, zero_global_t
-from ._train_abi import (ZERO_GLU_GELU, ZERO_GLU_SILU, ZERO_MAX_GROUPS, ZERO_STATE8_BLOCK, train_lib,
-                         zero_adam_group_t, zero_glu8_args, zero_linear8_args, zero_tensor_t,
-                         zero_tensors_args, zero_tensors_plan_t, zero_tensors_scalars_t, zero_xent_args,
-                         zero_xent_result_t)
+from ._train_abi import (ZERO_GLU_GELU, ZERO_GLU_SILU, ZERO_LINEAR8_BACKWARD, ZERO_LINEAR8_BACKWARD_ANY_DY,
+                         ZERO_LINEAR8_FORWARD, ZERO_MAX_GROUPS, ZERO_STATE8_BLOCK, train_lib, zero_adam_group_t,
+                         zero_glu8_args, zero_linear8_args, zero_tensor_t, zero_tensors_args, zero_tensors_plan_t,
+                         zero_tensors_scalars_t, zero_xent_args, zero_xent_result_t)
 
 
 def _on_device(**tensors) -> None:
@@ -570,8 +570,17 @@ def zero_glu8_backward(args: Glu8Args, stream=None) -> None:
 
 
 # ---------------------------------------------------------------- 8-bit products
-def zero_linear8_workspace_bytes(tokens: int, dim: int, out: int) -> int:
-    return train_lib().zero_linear8_workspace_bytes(tokens, dim, out)
+def zero_linear8_workspace_bytes(tokens: int, dim: int, out: int, forward: bool = True, backward: bool = True,
+                                 any_dy: bool = True) -> int:
+    """Bytes of workspace for calls of up to `tokens` tokens: of the forward,
+    of the backward, or of both.  Without any_dy the backward's dy has rows of
+    whole 16-byte pieces (16-byte aligned, out and the stride multiples of 8),
+    which it reads where they lie."""
+    uses = (ZERO_LINEAR8_FORWARD if forward else 0) | \
+        ((ZERO_LINEAR8_BACKWARD_ANY_DY if any_dy else ZERO_LINEAR8_BACKWARD) if backward else 0)
+    if not uses:
+        raise ValueError("a workspace for neither the forward nor the backward")
+    return train_lib().zero_linear8_workspace_bytes_for(tokens, dim, out, uses)
 
 
 @dataclass
