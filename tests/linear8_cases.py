@@ -1,9 +1,12 @@
 """Inputs of the 8-bit product whose results are exact, so that nothing is
 within a tolerance by being small: differences of the forward that are the
-gradient to the last bit but its own rounding."""
+gradient to the last bit but its own rounding, and whole sums that pass 2^24
+on the way to a small odd number, or end next to 2^31."""
 import torch
 
 import rows8_ref as ref
+
+LONGEST = 131071
 
 
 # ----------------------------------------------------------------- differences
@@ -39,3 +42,36 @@ def differences(forward, x8, xs, w8, ws, dy, k):
             codes[:, col] -= 1
         out.append(d)
     return out
+
+
+# ------------------------------------------------------------------ whole sums
+def whole(t, n, device, seed=0):
+    """(x8, x scales, w8, w scales, y): rows of LONGEST codes.  But for 81 places
+    x is 127 or -127 and w the same, of one sign in the first half and of the
+    other in the second, so a sum goes past 10^9 and back; at those places, in
+    both halves, both are odd and at most 3, so what is left is odd and at
+    most 729, a value of fp16.  The last token and the last channel are -128
+    all over: their own sum is 2^31 - 16384, held by a scale of 2^-26."""
+    g = torch.Generator().manual_seed(seed)
+    half = LONGEST // 2
+    few = torch.cat([torch.randperm(half, generator=g)[:40], half + torch.randperm(half, generator=g)[:40],
+                     torch.tensor([LONGEST - 1])]).to(device)
+
+    def codes(rows, turned):
+        q = torch.zeros(rows, ref.stride(LONGEST), dtype=torch.int8)
+        q = q.to(device)
+        sign = (torch.randint(0, 2, (rows, 1), generator=g) * 2 - 1).to(device)
+        q[:, :half] = (127 * sign).to(torch.int8)
+        q[:, half:LONGEST] = ((-127 if turned else 127) * sign).to(torch.int8)
+        odd = (torch.randint(-2, 2, (rows, 81), generator=g) * 2 + 1).to(device)
+        q[:, few] = odd.to(torch.int8)
+        q[-1, :LONGEST] = -128
+        return q, odd.double()
+    x8, xo = codes(t, False)
+    w8, wo = codes(n, True)
+    xs, ws = torch.ones(t, device=device), torch.ones(n, device=device)
+    ws[-1] = 2.0**-26
+    y = xo @ wo.t()
+    y[-1, :] = -128 * w8[:, :LONGEST].double().sum(1)
+    y[:, -1] = -128 * x8[:, :LONGEST].double().sum(1)
+    return x8, xs, w8, ws, y * ws.double()

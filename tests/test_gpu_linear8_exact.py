@@ -1,5 +1,6 @@
-"""The 8-bit product and its gradient on the exact cases of linear8_cases: the
-gradient against differences of the forward, element by element."""
+"""The 8-bit product and its gradient on the exact cases of linear8_cases: each
+kernel of the forward on whole sums far past 2^24, and the gradient against
+differences of the forward, element by element."""
 import pytest
 import torch
 
@@ -32,3 +33,19 @@ def test_gradient_is_the_forwards_differences(size, dtype):
         return y.clone()
     for got, want, what in zip((dx, dw), cases.differences(forward, x8, xs, w8, ws, dy, k), ("dx", "dw")):
         ref.within(got.double(), want, ref.half_step(want, dtype), what)
+
+
+@pytest.mark.parametrize("out", [20, 1040, 2050])
+@pytest.mark.parametrize("tokens", [1, 2, 20, 50, 200, 2049])
+def test_whole_sums(tokens, out):
+    """Past 10^9 and back to an odd number below 2^10, and 2^31 - 16384."""
+    say("linear8 whole sums %d x %d" % (tokens, out))
+    x8, xs, w8, ws, want = cases.whole(tokens, out, "cuda", seed=tokens + out)
+    y = torch.empty(tokens, out, dtype=torch.float16, device="cuda")
+    room = torch.empty(Z.zero_linear8_workspace_bytes(tokens, cases.LONGEST, out, backward=False), dtype=torch.uint8,
+                       device="cuda")
+    Z.zero_linear8_forward(Z.Linear8Args(x8, xs, w8, ws, dim=cases.LONGEST, workspace=room, y=y))
+    assert torch.equal(y[:-1, :-1].double(), want[:-1, :-1])
+    # of the rows of -128 the sum has up to 31 bits: fp32 and then fp16 round it
+    ref.within(y.double(), want, 3 * ref.U * want.abs() + ref.half_step(want, torch.float16), "y")
+    assert float(y[-1, -1]) == 32.0
