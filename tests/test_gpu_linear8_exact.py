@@ -35,8 +35,8 @@ def test_gradient_is_the_forwards_differences(size, dtype):
         ref.within(got.double(), want, ref.half_step(want, dtype), what)
 
 
-@pytest.mark.parametrize("out", [20, 1040, 2050])
-@pytest.mark.parametrize("tokens", [1, 2, 20, 50, 200, 2049])
+# of 4090 x 4090 the tiles are 256 x 256
+@pytest.mark.parametrize("tokens,out", [(t, n) for t in (1, 2, 20, 50, 200, 2049) for n in (20, 1040, 2050)] + [(4090, 4090)])
 def test_whole_sums(tokens, out):
     """Past 10^9 and back to an odd number below 2^10, and 2^31 - 16384."""
     say("linear8 whole sums %d x %d" % (tokens, out))
