@@ -49,4 +49,21 @@ int check_linear8_args(const zero_linear8_args* a, bool backward);
 // Bytes of workspace that this call uses; 0 for out-of-range sizes.
 size_t linear8_needs(const zero_linear8_args* a, bool backward);
 
+// How `most` blocks are shared by two lists of tiles, one a block where there
+// are no more than that, else by their work (of a tile: work_a and work_b).
+inline void share_blocks(int64_t a, int64_t b, double work_a, double work_b, int64_t most, int64_t* first,
+                         int64_t* second) {
+    *first = a;
+    *second = b;
+    if (a + b <= most) return;
+    const double wa = static_cast<double>(a) * work_a, wb = static_cast<double>(b) * work_b;
+    *first = a == 0 ? 0 : (b == 0 ? most : static_cast<int64_t>(static_cast<double>(most) * (wa / (wa + wb)) + 0.5));
+    if (a > 0 && *first < 1) *first = 1;
+    if (b > 0 && *first > most - 1) *first = most - 1;
+    // what one has no tile for is the other's (gradient of 128 tokens x 512 x 16384 27.9 us, left idle 30.2)
+    if (*first > a) *first = a;
+    *second = most - *first < b ? most - *first : b;
+    *first = most - *second < a ? most - *second : a;
+}
+
 }  // namespace zero

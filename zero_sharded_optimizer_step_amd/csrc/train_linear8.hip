@@ -880,23 +880,14 @@ void place(Product* q, int slices, float* slabs, int64_t ld, int64_t rows, int64
 
 // dx's and dw's tiles of 128 x 128 in one grid, either may have none: each
 // leaves CUs idle by itself (509 tokens x 1000 x 2053 in fp16 13 and 9 us one
-// after the other).  Where there are more than the CUs take at once, each gets
-// blocks by its share of the work.
+// after the other).
 template <int DT>
 void two_products(Product a, Product b, hipStream_t st) {
     a.tiles_m = (a.m + 127) / 128;
     b.tiles_m = (b.m + 127) / 128;
     const int64_t na = tiles_of(a, 128, 128) * a.slices, nb = tiles_of(b, 128, 128) * b.slices;
-    int64_t first = na, second = nb;
-    if (na + nb > kTilesAtOnce) {
-        const double wa = static_cast<double>(na) * (a.slice + kTileK), wb = static_cast<double>(nb) * (b.slice + kTileK);
-        first = na == 0 ? 0 : (nb == 0 ? kTilesAtOnce : static_cast<int64_t>(kTilesAtOnce * (wa / (wa + wb)) + 0.5));
-        if (na > 0 && first < 1) first = 1;
-        if (nb > 0 && first > kTilesAtOnce - 1) first = kTilesAtOnce - 1;
-        second = kTilesAtOnce - first;
-        if (first > na) first = na;
-        if (second > nb) second = nb;
-    }
+    int64_t first, second;
+    share_blocks(na, nb, a.slice + kTileK, b.slice + kTileK, kTilesAtOnce, &first, &second);
     hipLaunchKernelGGL((two_products_kernel<DT, kEither, 128, 128, 2, 2>), dim3(static_cast<unsigned>(first + second)),
                        dim3(256), 0, st, a, b, static_cast<int>(first));
 }
