@@ -95,3 +95,20 @@ def test_beside_a_nan_and_in_rows_read_twice(kind, width):
     assert torch.equal(c.h[:, rest], plain[:, rest])
     c.same_codes(c.h8[:2], c.h_scale[:2], c.h[:2], "h8")
     assert bool(torch.isnan(c.h_scale[2]))
+
+
+@pytest.mark.parametrize("gated", [True, False], ids=["gated", "plain"])
+@pytest.mark.parametrize("kind", ["silu", "gelu"])
+def test_a_scale_may_be_negative(kind, gated):
+    """Codes and scales of the other sign stand for the same gates."""
+    say("glu8 low end, negative scales %s %s" % (kind, gated))
+    c = call(kind, torch.bfloat16, gated, 1.0)
+    Z.zero_glu8_forward(c.args)
+    Z.zero_glu8_backward(c.args)
+    want = [m.clone() for m in (c.dgate, c.dup) if m is not None]
+    assert int((want[0] != 0).sum()) > 24 * 100
+    c.gate8.neg_()
+    c.gate_scale.neg_()
+    Z.zero_glu8_backward(c.args)
+    for got, w in zip((c.dgate, c.dup), want):
+        assert torch.equal(got, w)

@@ -471,7 +471,7 @@ __global__ __launch_bounds__(256) void glu8_backward_kernel(const Glu q) {
     for (int64_t r = static_cast<int64_t>(blockIdx.x / q.parts) * kRowsABlock<TR> + threadIdx.x / TR; r < q.tokens;
          r += static_cast<int64_t>(gridDim.x / q.parts) * kRowsABlock<TR>) {
         const float sg = q.gate_scale[r], su = kGated ? q.up_scale[r] : 1.0f;
-        const bool far = far_gate<DT, KIND>(128.0f * sg);
+        const bool far = far_gate<DT, KIND>(128.0f * __builtin_fabsf(sg));
         const char *gate8 = q.gate8 + r * q.gate8_row, *up8 = kGated ? q.up8 + r * q.up8_row : nullptr;
         const char* dh = q.dh + r * q.dh_row;
         Piece<DT> p[P];
