@@ -70,3 +70,17 @@ def test_what_a_call_does_not_use_is_not_asked_for():
     Z.zero_linear8_backward(want.args)
     assert torch.equal(c.db, want.db)
     margin_untouched(whole, less)
+
+
+def test_nothing_of_rows_far_apart():
+    """No output channel, or no token, of a dy of any stride: zeros."""
+    for t, k, n in ((3, 40, 0), (200, 300, 0), (0, 40, 30)):
+        for stride in (1 << 25, (1 << 25) + 8, (1 << 20) + 1):
+            say("linear8 nothing of %s, %d apart" % ((t, k, n), stride))
+            c = Call(t, k, n, torch.bfloat16)
+            rows = torch.empty(min(t, 3) * stride, dtype=torch.bfloat16, device="cuda")
+            # no element of a row exists, so three rows' memory does for all
+            c.args.dy = rows.as_strided((t, n), (stride, 1)) if n == 0 else c.dy
+            Z.zero_linear8_backward(c.args)
+            assert not bool(c.dx.any()) and not bool(c.dw.any()) and not bool(c.db.any())
+            c.clean()

@@ -941,7 +941,7 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
     float* part = dw_slab + c.dw_slab / 4;
     const int64_t t = a->tokens, n = a->out;
     const bool want_dx = a->dx && t > 0 && a->dim > 0, want_dw = a->dw && n > 0 && a->dim > 0, want_db = a->db && n > 0;
-    const bool repack = copies_dy(a);
+    const bool whole = whole_pieces(a->dy, a->dy_stride, n), repack = copies_dy(a);
     const int64_t dyr_ld = up(n, 64);
     const int64_t last = want_dx || want_dw ? a->dim : 1;   // db alone: once
     for (int64_t d = 0; d < last; d += c.piece) {
@@ -979,9 +979,10 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
             q->a = reinterpret_cast<const char*>(held16);
             q->lda = c.piece * 2;
             q->m = static_cast<int32_t>(up(wide, 8));
-            // no row or no column: nothing of dy is read
-            q->b = repack ? reinterpret_cast<const char*>(dyr) : static_cast<const char*>(a->dy);
-            q->ldb = (repack ? dyr_ld : a->dy_stride) * 2;
+            // No row or no column: nothing of dy is read, nor of a copy that is not
+            // made; but rows of any stride would lead kNowhere back into range.
+            q->b = whole ? static_cast<const char*>(a->dy) : reinterpret_cast<const char*>(dyr);
+            q->ldb = (whole ? a->dy_stride : dyr_ld) * 2;
         };
         if (want_dx) {
             unsigned short* out = static_cast<unsigned short*>(a->dx) + d;
