@@ -1,6 +1,8 @@
 """The 8-bit product in a workspace of a larger batch, of the forward alone,
 and of a gradient without a copy of dy: the results are those of a workspace
 of its own, and nothing past its end is written."""
+import re
+
 import pytest
 import torch
 
@@ -70,6 +72,31 @@ def test_what_a_call_does_not_use_is_not_asked_for():
     Z.zero_linear8_backward(want.args)
     assert torch.equal(c.db, want.db)
     margin_untouched(whole, less)
+
+
+@pytest.mark.parametrize("wanted", [("dx",), ("dw",), ("db",), ("dx", "dw"), ("dx", "db"), ("dw", "db")], ids="+".join)
+def test_a_part_of_the_gradient_in_its_own_room(wanted):
+    """Each gradient needs its own operand's room alone."""
+    for size in ((20, 300, 500), (64, 2048, 1100), (300, 512, 264), (700, 1000, 333), (2100, 520, 2304)):
+        for pad in (0, 1):
+            say("linear8 workspace of %s %s %d" % (wanted, size, pad))
+            c = Call(*size, torch.bfloat16, pad=pad)
+            Z.zero_linear8_backward(c.args)
+            want = {name: getattr(c, name).clone() for name in wanted}
+            for name in ("dx", "dw", "db"):
+                getattr(c, name).fill_(-7)
+                if name not in wanted:
+                    setattr(c.args, name, None)
+            with pytest.raises(Z.ZeroError, match="workspace_bytes") as refused:
+                c.args.workspace = c.room[:1]
+                Z.zero_linear8_backward(c.args)
+            size_needed = int(re.search(r"< (\d+) needed", str(refused.value)).group(1))
+            whole, c.args.workspace = room(size_needed)
+            Z.zero_linear8_backward(c.args)
+            for name in ("dx", "dw", "db"):
+                assert torch.equal(getattr(c, name), want[name]) if name in wanted else bool((getattr(c, name) == -7).all())
+            margin_untouched(whole, size_needed)
+            c.clean()
 
 
 def test_nothing_of_rows_far_apart():

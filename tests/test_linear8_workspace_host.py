@@ -5,6 +5,7 @@ they lie for no copy of them.  On the CPU: a call that is refused names what
 it needs before anything is launched."""
 import ctypes
 import re
+import time
 
 import pytest
 
@@ -75,8 +76,17 @@ def test_what_is_not_needed_is_not_asked_for():
     assert SIZE(8192, 4096, 16384) - SIZE(8192, 4096, 16384, any_dy=False) == copy
     # rows off their alignment, as columns of a wider matrix
     assert needs("backward", 8192, 4096, 16384, dy=A + 2) == anywhere
-    # the column sums alone read dy where it lies
-    assert needs("backward", 8192, 4096, 16384, whole=False, dx=None, dw=None) <= whole
+    # the column sums alone read dy where it lies and need 16 shares of them; each product its own operand
+    assert needs("backward", 8192, 4096, 16384, whole=False, dx=None, dw=None) == 16 * 16384 * 4
+    dx, dw = (needs("backward", 8192, 4096, 16384, **{other: None, "db": None}) for other in ("dw", "dx"))
+    assert (dx, dw) == (16384 * 4096 * 2, 8192 * 4096 * 2) and whole == dx + dw + 16 * 16384 * 4
+
+
+def test_the_query_is_quick_where_nothing_is_needed():
+    start = time.perf_counter()
+    for sizes in ((1 << 20, 131071, 0), (1 << 20, 0, 1 << 20), (1 << 20, 131071, 1), (0, 131071, 1 << 20)):
+        assert SIZE(*sizes) >= 256
+    assert time.perf_counter() - start < 1
 
 
 def test_uses():

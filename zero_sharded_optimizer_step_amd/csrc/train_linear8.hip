@@ -615,8 +615,21 @@ constexpr int64_t kCacheBytes = int64_t(256) << 20;
 constexpr int64_t kMostPacks = 1 << 22;       // blocks; with the others' the grid's 32 bits hold them
 constexpr size_t kPieceBytes = size_t(512) << 20;
 
-// How a gradient is cut: by the three sizes alone.  Its workspace has a copy of
-// dy's rows besides, where they are not read as they lie.
+// What a gradient's call has to make, a copy of dy's rows among it where they
+// are not read as they lie.
+struct Wanted {
+    bool dx, dw, db, copy_dy;
+};
+Wanted wanted(const zero_linear8_args* a) {
+    Wanted w;
+    w.dx = a->dx && a->tokens > 0 && a->dim > 0;
+    w.dw = a->dw && a->out > 0 && a->dim > 0;
+    w.db = a->db && a->out > 0;
+    w.copy_dy = (w.dx || w.dw) && a->tokens > 0 && a->out > 0 && !whole_pieces(a->dy, a->dy_stride, a->out);
+    return w;
+}
+
+// How a gradient is cut: by the three sizes alone; and its workspace.
 struct Cut {
     int64_t piece;            // columns of dim at a time, a multiple of 256
     int32_t dx_slices, dw_slices;
@@ -645,7 +658,7 @@ bool in_range(int64_t tokens, int64_t dim, int64_t out) {
     return tokens >= 0 && tokens <= kMaxTokens && dim >= 0 && dim <= ZERO_ROWS8_MAX_DIM && out >= 0 && out <= kMaxOut;
 }
 
-bool cut(int64_t tokens, int64_t dim, int64_t out, bool copy_dy, Cut* c) {
+bool cut(int64_t tokens, int64_t dim, int64_t out, const Wanted& want, Cut* c) {
     if (!in_range(tokens, dim, out)) return false;
     const int64_t t = tokens > 0 ? tokens : 1, k = up(dim > 0 ? dim : 1, 256), n = out > 0 ? out : 1;
     int64_t piece = static_cast<int64_t>(kPieceBytes / (2 * static_cast<size_t>(t + n))) / 256 * 256;
@@ -663,22 +676,24 @@ bool cut(int64_t tokens, int64_t dim, int64_t out, bool copy_dy, Cut* c) {
     int64_t shares = 1024 / columns;
     if (shares > t / 64) shares = t / 64;
     c->shares = static_cast<int32_t>(shares < 1 ? 1 : shares);
-    c->x_bytes = round_up(static_cast<size_t>(t * c->piece) * 2, 256);
-    c->w_bytes = round_up(static_cast<size_t>(n * c->piece) * 2, 256);
-    c->dy_bytes = copy_dy ? round_up(static_cast<size_t>(t * up(n, 64)) * 2, 256) : 0;
-    c->dx_slab = c->dx_slices > 1 ? round_up(static_cast<size_t>(c->dx_slices) * t * c->piece * 4, 256) : 0;
-    c->dw_slab = c->dw_slices > 1 ? round_up(static_cast<size_t>(c->dw_slices) * n * c->piece * 4, 256) : 0;
-    c->part_bytes = round_up(static_cast<size_t>(c->shares) * n * 4, 256);
+    auto bytes = [](bool needed, int64_t count, size_t of) {
+        return needed ? round_up(static_cast<size_t>(count) * of, 256) : size_t(0);
+    };
+    c->x_bytes = bytes(want.dw, t * c->piece, 2);
+    c->w_bytes = bytes(want.dx, n * c->piece, 2);
+    c->dy_bytes = bytes(want.copy_dy, t * up(n, 64), 2);
+    c->dx_slab = bytes(want.dx && c->dx_slices > 1, c->dx_slices * t * c->piece, 4);
+    c->dw_slab = bytes(want.dw && c->dw_slices > 1, c->dw_slices * n * c->piece, 4);
+    c->part_bytes = bytes(want.db && c->shares > 1, c->shares * n, 4);
     c->total = c->x_bytes + c->w_bytes + c->dy_bytes + c->dx_slab + c->dw_slab + c->part_bytes;
     // one or two blocks a CU, a step or more for each of their waves
     int64_t few = kCus * (t <= 16 ? 2 : 1) / (up(k, kFewColumns) / kFewColumns);
     if (few > n / (kGradientWaves * kFewRows)) few = n / (kGradientWaves * kFewRows);
     c->few_shares = static_cast<int32_t>(few < 1 ? 1 : few);
     if (few_gradient_rule(t, dim, n)) {
-        // nothing is written out in 16 bits; db alone may still be asked for
+        // nothing is written out in 16 bits, and db is one share's
         c->x_bytes = c->w_bytes = c->dy_bytes = c->dx_slab = c->dw_slab = 0;
-        const size_t sums = round_up(static_cast<size_t>(c->few_shares) * t * up(k, 8) * 4, 256);
-        c->total = c->part_bytes > sums ? c->part_bytes : sums;
+        c->total = bytes(want.dx && c->few_shares > 1, c->few_shares * t * k, 4);
     }
     return true;
 }
@@ -769,9 +784,9 @@ size_t forward_bytes(int64_t tokens, int64_t dim, int64_t out) {
     const size_t sums = slices > 1 ? static_cast<size_t>(slices) * tokens * up(out, 64) * 4 : 0;
     return sums > kLeastBytes ? round_up(sums, 256) : kLeastBytes;
 }
-size_t backward_bytes(int64_t tokens, int64_t dim, int64_t out, bool copy_dy) {
+size_t backward_bytes(int64_t tokens, int64_t dim, int64_t out, const Wanted& want) {
     Cut c;
-    if (!cut(tokens, dim, out, copy_dy, &c)) return 0;
+    if (!cut(tokens, dim, out, want, &c)) return 0;
     return c.total > kLeastBytes ? c.total : kLeastBytes;
 }
 
@@ -779,6 +794,7 @@ size_t backward_bytes(int64_t tokens, int64_t dim, int64_t out, bool copy_dy) {
 // into more slices, or have wider pieces of columns.
 size_t most_forward_bytes(int64_t tokens, int64_t dim, int64_t out) {
     size_t most = kLeastBytes;
+    if (out == 0) return most;
     // none with more tiles than half of the chip's is cut
     for (int64_t t = 1; t <= tokens && 2 * (up(t, 128) / 128) * (up(out, 128) / 128) <= kTilesAtOnce; ++t) {
         const size_t b = forward_bytes(t, dim, out);
@@ -787,13 +803,14 @@ size_t most_forward_bytes(int64_t tokens, int64_t dim, int64_t out) {
     return most;
 }
 size_t most_backward_bytes(int64_t tokens, int64_t dim, int64_t out, bool copy_dy) {
-    size_t most = backward_bytes(tokens, dim, out, copy_dy);
+    const Wanted all = {true, true, true, copy_dy};
+    size_t most = backward_bytes(tokens, dim, out, all);
     // Between two of these nothing but the tokens grows: rules end at 16, 32 and
     // 64, tiles and shares change at multiples of 64 or behind them, and a
     // narrower piece begins where its width no longer divides kPieceBytes so.
     auto look = [&](int64_t t) {
         if (t < 1 || t >= tokens) return;
-        const size_t b = backward_bytes(t, dim, out, copy_dy);
+        const size_t b = backward_bytes(t, dim, out, all);
         most = b > most ? b : most;
     };
     look(16);
@@ -806,12 +823,6 @@ size_t most_backward_bytes(int64_t tokens, int64_t dim, int64_t out, bool copy_d
     for (int64_t wide = 256; wide <= up(dim, 256); wide += 256)
         look(static_cast<int64_t>(kPieceBytes) / 2 / wide - n);
     return most;
-}
-
-// Whether the products need a copy of dy's rows.
-bool copies_dy(const zero_linear8_args* a) {
-    const bool any = a->dim > 0 && ((a->dx && a->tokens > 0) || (a->dw && a->out > 0));
-    return any && a->tokens > 0 && a->out > 0 && !whole_pieces(a->dy, a->dy_stride, a->out);
 }
 
 template <int OT>
@@ -929,7 +940,7 @@ int few_gradient(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
 }
 
 template <int DT>
-int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
+int backward(const zero_linear8_args* a, const Wanted& want, const Cut& c, hipStream_t st) {
     if (a->tokens > 0 && a->dim > 0 && (a->dx || a->dw) && few_gradient_rule(a->tokens, a->dim, a->out))
         return few_gradient<DT>(a, c, st);
     char* ws = static_cast<char*>(a->workspace);
@@ -940,10 +951,9 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
     float* dw_slab = dx_slab + c.dx_slab / 4;
     float* part = dw_slab + c.dw_slab / 4;
     const int64_t t = a->tokens, n = a->out;
-    const bool want_dx = a->dx && t > 0 && a->dim > 0, want_dw = a->dw && n > 0 && a->dim > 0, want_db = a->db && n > 0;
-    const bool whole = whole_pieces(a->dy, a->dy_stride, n), repack = copies_dy(a);
+    const bool whole = whole_pieces(a->dy, a->dy_stride, n);
     const int64_t dyr_ld = up(n, 64);
-    const int64_t last = want_dx || want_dw ? a->dim : 1;   // db alone: once
+    const int64_t last = want.dx || want.dw ? a->dim : 1;   // db alone: once
     for (int64_t d = 0; d < last; d += c.piece) {
         const int64_t wide = a->dim - d < c.piece ? a->dim - d : c.piece;
         Prepare p = {};
@@ -966,11 +976,11 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
         p.past = n >= 8 && t * n * 2 >= kCacheBytes;
         p.part = part;
         p.db = c.shares == 1 ? static_cast<unsigned short*>(a->db) : nullptr;
-        p.ends[0] = d == 0 && want_db ? static_cast<uint32_t>(p.column_blocks * c.shares) : 0;
-        p.ends[1] = p.ends[0] + (want_dx ? held(&p.held[0], a->w8, a->w8_stride, a->w_scale, n, w16) : 0);
-        p.ends[2] = p.ends[1] + (want_dw ? held(&p.held[1], a->x8, a->x8_stride, a->x_scale, t, x16) : 0);
+        p.ends[0] = d == 0 && want.db ? static_cast<uint32_t>(p.column_blocks * c.shares) : 0;
+        p.ends[1] = p.ends[0] + (want.dx ? held(&p.held[0], a->w8, a->w8_stride, a->w_scale, n, w16) : 0);
+        p.ends[2] = p.ends[1] + (want.dw ? held(&p.held[1], a->x8, a->x8_stride, a->x_scale, t, x16) : 0);
         const int64_t packs = (t * (dyr_ld / 8) + 255) / 256;
-        p.ends[3] = p.ends[2] + (d == 0 && repack ? static_cast<uint32_t>(packs < kMostPacks ? packs : kMostPacks) : 0);
+        p.ends[3] = p.ends[2] + (d == 0 && want.copy_dy ? static_cast<uint32_t>(packs < kMostPacks ? packs : kMostPacks) : 0);
         if (p.ends[3] > 0) hipLaunchKernelGGL((prepare_kernel<DT>), dim3(p.ends[3]), dim3(256), 0, st, p);
 
         Finish f = {};
@@ -984,7 +994,7 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
             q->b = whole ? static_cast<const char*>(a->dy) : reinterpret_cast<const char*>(dyr);
             q->ldb = (whole ? a->dy_stride : dyr_ld) * 2;
         };
-        if (want_dx) {
+        if (want.dx) {
             unsigned short* out = static_cast<unsigned short*>(a->dx) + d;
             both(&dx, w16);
             dx.n = static_cast<int32_t>(t);
@@ -994,7 +1004,7 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
             f.ends[0] = c.dx_slices > 1 ? static_cast<uint32_t>((t * (c.piece / 4) + 255) / 256) : 0;
         }
         f.ends[1] = f.ends[0];
-        if (want_dw) {
+        if (want.dw) {
             unsigned short* out = static_cast<unsigned short*>(a->dw) + d;
             both(&dw, x16);
             dw.n = static_cast<int32_t>(n);
@@ -1007,13 +1017,13 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
         f.out = n;
         f.shares = c.shares;
         f.db = static_cast<unsigned short*>(a->db);
-        f.ends[2] = f.ends[1] + (d == 0 && want_db && c.shares > 1 ? static_cast<uint32_t>((n + 255) / 256) : 0);
+        f.ends[2] = f.ends[1] + (d == 0 && want.db && c.shares > 1 ? static_cast<uint32_t>((n + 255) / 256) : 0);
         // more than one slice only where they are one round of the small tiles
-        const bool large_dx = want_dx && c.dx_slices == 1 && large_tiles(dx, 1);
-        const bool large_dw = want_dw && c.dw_slices == 1 && large_tiles(dw, 1);
+        const bool large_dx = want.dx && c.dx_slices == 1 && large_tiles(dx, 1);
+        const bool large_dw = want.dw && c.dw_slices == 1 && large_tiles(dw, 1);
         if (large_dx) launch_tiles<DT, kCols, kRows, kPlain, 256, 256, 2, 2>(dx, 1, st);
         if (large_dw) launch_tiles<DT, kCols, kCols, kPlain, 256, 256, 2, 2>(dw, 1, st);
-        if ((want_dx && !large_dx) || (want_dw && !large_dw))
+        if ((want.dx && !large_dx) || (want.dw && !large_dw))
             two_products<DT>(large_dx ? Product{} : dx, large_dw ? Product{} : dw, st);
         if (f.ends[2] > 0) hipLaunchKernelGGL((finish_kernel<DT>), dim3(f.ends[2]), dim3(256), 0, st, f);
     }
@@ -1024,7 +1034,7 @@ int backward(const zero_linear8_args* a, const Cut& c, hipStream_t st) {
 
 size_t linear8_needs(const zero_linear8_args* a, bool backward) {
     if (!in_range(a->tokens, a->dim, a->out)) return 0;
-    return backward ? backward_bytes(a->tokens, a->dim, a->out, copies_dy(a)) : forward_bytes(a->tokens, a->dim, a->out);
+    return backward ? backward_bytes(a->tokens, a->dim, a->out, wanted(a)) : forward_bytes(a->tokens, a->dim, a->out);
 }
 
 }  // namespace zero
@@ -1060,10 +1070,11 @@ int zero_linear8_backward(const zero_linear8_args* a, void* stream) {
     clear_error();
     const int rc = check_linear8_args(a, true);
     if (rc || (a->tokens == 0 && a->out == 0)) return rc;
+    const Wanted want = wanted(a);
     Cut c;
-    cut(a->tokens, a->dim, a->out, copies_dy(a), &c);
+    cut(a->tokens, a->dim, a->out, want, &c);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return a->dtype == ZERO_BF16 ? backward<ZERO_BF16>(a, c, st) : backward<ZERO_FP16>(a, c, st);
+    return a->dtype == ZERO_BF16 ? backward<ZERO_BF16>(a, want, c, st) : backward<ZERO_FP16>(a, want, c, st);
 }
 
 }  // extern "C"
