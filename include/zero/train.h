@@ -397,8 +397,8 @@ typedef struct {
  * backward has in it at most 512 MB of x^ and w^ in 16 bits (of 256 columns,
  * if that is more), fp32 parts of dx and dw where their sums are cut (34 MB
  * each), shares of db's sum, and a copy of dy, 2 tokens out bytes, where its
- * rows are not read as they lie.  Of few tokens it has parts of dx's sums or
- * shares of db's alone.
+ * rows are not read as they lie; a call that wants fewer of dx, dw and db has
+ * their parts alone.  Of few tokens it has parts of dx's sums, or nothing.
  * 0 for out-of-range sizes or uses.  Host only; a search over the numbers of
  * tokens, 10 us to 1 ms. */
 #define ZERO_LINEAR8_FORWARD 1
@@ -416,8 +416,9 @@ size_t zero_linear8_workspace_bytes(int64_t tokens, int64_t dim, int64_t out);
 int zero_linear8_forward(const zero_linear8_args* a, void* stream);
 
 /* Writes those of dx, dw and db that are given from dy, w8 (dx) and x8 (dw)
- * with their scales; bias and y are not used.  No token: dw and db are zero;
- * no output channel: dx is zero.  Errors as above. */
+ * with their scales; bias and y are not used.  No output may overlap an input
+ * or another output.  No token: dw and db are zero; no output channel: dx is
+ * zero.  Errors as above. */
 int zero_linear8_backward(const zero_linear8_args* a, void* stream);
 
 #ifdef __cplusplus

@@ -341,9 +341,10 @@ __global__ __launch_bounds__(256) void finish_kernel(const Finish q) {
 // second kernel, or where there is one share that is dx.
 // Of 4096 x 16384 1 token takes 46 us (4.4 TB/s of w8 and dw), 16 49, 32 54 and
 // 64 63: 8 us more of products and conversions, 4 of joining.  Up to 16 tokens
-// two blocks share a CU (16 tokens: one 54).  Neighbouring columns' blocks run
-// on unlike XCDs; the other way round 1 token takes 52.  w8 read past the
-// caches: 47; dw written through them: 50.
+// two blocks share a CU (16 tokens: one 54).  33 to 48 tokens have a form of
+// their own: 48 take 57.4 us, by that of 64 59.1, of 4096 x 4096 19.5 and 20.4.
+// Neighbouring columns' blocks run on unlike XCDs; the other way round 1 token
+// takes 52.  w8 read past the caches: 47; dw written through them: 50.
 struct FewGradient {
     const char* w8;
     const char* x8;
@@ -642,11 +643,11 @@ struct Cut {
 // Whether few_gradient_kernel takes it: up to 32 tokens, and up to 64 of weights
 // that are not small, where the tiles' three launches are the shorter chain.
 // Microseconds, and those of the tiles: 64 tokens x 4096 x 16384 63 and 125, x
-// 1024 x 16384 26 and 44, x 1000 x 4100 16.8 and 18.7, x 2048 x 1000 15.6 and
-// 16.8, but x 1000 x 2053 18.7 and 16.5, x 200 x 300 12.7 and 9.5; 32 tokens x
-// 1000 x 2053 14.1 and 15.8, x 200 x 300 9.3 and 9.2; 16 x 200 x 300 8.1 and
-// 9.2, x 64 x 64 5.9 and 7.3; 1 x 1000 x 4100 11.6, where a kernel without
-// matrix cores took 10.6, but x 64 x 64 5.7 and 7.0.
+// 1024 x 16384 26 and 44, x 1000 x 4100 16.8 and 18.7, but x 1000 x 2053 18.7 and
+// 16.5, x 200 x 300 12.7 and 9.5; x 2048 x 1000, 15.6 and 16.8, goes by the tiles
+// all the same.  32 tokens x 1000 x 2053 14.1 and 15.8, x 200 x 300 9.3 and 9.2;
+// 16 x 200 x 300 8.1 and 9.2, x 64 x 64 5.9 and 7.3; 1 x 1000 x 4100 11.6, where
+// a kernel without matrix cores took 10.6, but x 64 x 64 5.7 and 7.0.
 constexpr int64_t kFewGradientTokens = 32, kMoreGradientTokens = 64, kMoreWeights = int64_t(1) << 21;
 bool few_gradient_rule(int64_t tokens, int64_t dim, int64_t out) {
     // a row of dy has whole pieces to take its end out of
@@ -718,7 +719,8 @@ void few(const Few& q, hipStream_t st) {
 // 256 tokens x 4096 x 4096 23.0, 20.1, 18.7, 18.5, 23.0 (3); 256 x 16384 x 4096
 // 67.5, 46.6, 37.4 (46 elsewhere in memory), 40.2, 39.6 (3); 512 x 4096 x 4096
 // 23.5, 24.6, 26.6, 27.3, 43.9 (1); 700 x 8000 x 1500 43.3, 31.8, 26.4, 28.9,
-// 32.8 (3).
+// 32.8 (3).  It is not always the best: 512 x 16384 x 4096 71.2, 65.0, 61.9, 56.5,
+// 70.2 (2), 1500 x 16000 x 600 72.7, 45.9, 36.0, 33.0, 34.0 (3).
 int forward_slices(int64_t tokens, int64_t dim, int64_t out) {
     const int64_t tiles = up(tokens, 128) / 128 * (up(out, 128) / 128), steps = up(dim, 128) / 128;
     const double operands = static_cast<double>(tiles) * 256.0 * static_cast<double>(dim) * 1e-7;

@@ -72,8 +72,8 @@ __device__ __forceinline__ void value4(unsigned codes, float s, float o[4]) {
 // -------------------------------------------------------------------- pieces
 // All of it is read and written once: past the caches' own order of keeping,
 // a large call leaves to them what its caller has there.  Of 8192 x 16384 in
-// bf16 the gated forward takes 162 us so and 170 without, its backward 177 and
-// 200; 16384 x 4096 encoded 35.6 and 36.9.
+// bf16 the gated forward takes 165 us so and 182 without, its backward 168 and
+// 186; 16384 x 4096 encoded 37.7 and 38.9, read back 37.1 and 38.9.
 template <typename T>
 __device__ __forceinline__ void put(void* at, T v) {
     __builtin_nontemporal_store(v, static_cast<T*>(at));
@@ -321,8 +321,8 @@ constexpr float kCubic = 0.044715f;
 // 2^-z there, as far as fp32 has it, and the same bits everywhere else.  It
 // costs 3 % where it runs for all, so rows that have no such gate go without:
 // far_gate().  Of 8192 x 16384 silu's gated forward takes 171 us either way on
-// values of a normal distribution and 162 and 175 on rows that all have far
-// gates; alone 97 and 103, gelu's alone 100 and 110.
+// values of a normal distribution and 162 and 169 on rows that all have far
+// gates; alone 97 and 105, gelu's alone 100 and 115.
 // Beyond 16 gelu's p is 0 or 1 in fp32, so its argument stops there: no power
 // of a large x overflows.  A NaN x gives NaN.
 template <int KIND, bool kLow>
@@ -531,10 +531,18 @@ unsigned row_blocks(int64_t rows, int64_t parts = 1) {
     return static_cast<unsigned>(b < most ? b : most);
 }
 
-// The threads and pieces of a row for the encoders, by its length.  Of 16384
-// elements 512 threads hold two parts, gate and up (8192 rows forward 163 us;
-// 256, with 236 registers each, 175), and 256 one (4096 rows of gelu 64.5 us,
-// 512 72).
+// The threads and pieces of a row for the encoders, by its length: the fewest
+// that hold it.  Microseconds, and with those of the next longer rows, bf16:
+// 100000 x 128 encoded 10.0 and 27, 50000 x 128 gated forward 12.7 and 35; 65536
+// x 512 24.5 and 30, 32768 x 512 26.7 and 43; 16384 x 2048 19.1 and 23.9, 8192 x
+// 2048 24.7 and 28.0; 16384 x 4096 37.6 and 38.5, 8192 x 4096 42 and 53; 8192 x
+// 8192 36.5 and 36.4, 4096 x 8192 44 and 56; 4096 x 16384 37.5 and 55 (as rows
+// read twice), 2048 x 16384 45 and 76.  Of 16384 elements 512 threads hold two
+// parts, gate and up (8192 rows forward 163 us; 256, with 236 registers each,
+// 175), and 256 one (4096 rows of gelu 64.5 us, 512 72).
+// Short rows, one load a wave between maximum and codes, reach 3.6 to 4.1 TB/s
+// (200000 x 64, 65536 x 512, 16384 x 1024).  Rows past 16384 are read twice: 2000
+// x 40000 59.5 us (4.0 TB/s), 4096 x 28672 gated forward 197 (4.2).
 template <int DT, int kParts, typename F>
 void by_row(int64_t dim, const F& f) {
     using std::integral_constant;
@@ -548,7 +556,14 @@ void by_row(int64_t dim, const F& f) {
     else if (eights <= 2048) f(integral_constant<int, 256 * kParts>{}, integral_constant<int, 8 / kParts * kMore>{}, std::true_type{});
     else f(integral_constant<int, 1024>{}, integral_constant<int, 4 * kMore>{}, std::false_type{});
 }
-// And for the readers, whose blocks take part of a row.
+// And for the readers, whose blocks take part of a row.  Microseconds, bf16,
+// with 8 and 64 threads a row: 200000 x 64 read back 9.6 and 37, 100000 x 64 gated
+// gradient 12.6 and 52; with 64 and 256: 65536 x 512 20.5 and 44, 32768 x 512 25
+// and 61, 16384 x 4096 36.4 and 35.5, 8192 x 4096 plain gradient 38 and 31.7.
+// From 513 to about 2048 elements, where 256 threads have less than a piece each
+// to do, 64 are the faster, which the rule does not take: 32768 x 600 18.9 and
+// 27.3, 16384 x 600 gated gradient 22 and 37, 8192 x 1024 14.3 and 20.6, x 2048
+// 25.0 and 27.3.
 template <int DT, typename F>
 void by_piece(int64_t dim, const F& f) {
     using std::integral_constant;
