@@ -97,5 +97,7 @@ def test_uses():
         each = [of(*sizes, uses) for uses in (1, 2, 4)]
         assert all(e >= 256 and e % 256 == 0 for e in each)
         assert of(*sizes, 7) == max(each) == SIZE(*sizes)
+        named = (Z.ZERO_LINEAR8_FORWARD, Z.ZERO_LINEAR8_BACKWARD, Z.ZERO_LINEAR8_BACKWARD_ANY_DY)
+        assert [Z.zero_linear8_workspace_bytes_for(*sizes, uses) for uses in named] == each
     with pytest.raises(ValueError):
         SIZE(100, 100, 100, forward=False, backward=False)

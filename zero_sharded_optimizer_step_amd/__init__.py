@@ -45,7 +45,9 @@ __all__ = [
     "zero_xent_workspace_bytes", "zero_xent_forward", "zero_xent_backward",
     "rows8_stride", "zero_rows8_encode", "zero_rows8_decode", "ZERO_GLU_SILU", "ZERO_GLU_GELU",
     "Glu8Args", "zero_glu8_forward", "zero_glu8_backward", "Linear8Args",
-    "zero_linear8_workspace_bytes", "zero_linear8_forward", "zero_linear8_backward",
+    "ZERO_LINEAR8_FORWARD", "ZERO_LINEAR8_BACKWARD", "ZERO_LINEAR8_BACKWARD_ANY_DY",
+    "zero_linear8_workspace_bytes", "zero_linear8_workspace_bytes_for", "zero_linear8_forward",
+    "zero_linear8_backward",
 ]
 
 GLOBAL_BYTES = ctypes.sizeof(zero_global_t)
@@ -535,11 +537,12 @@ def zero_gather_params(part: zero_partition_t, shards: Sequence, dtype, lo: int,
 
 # ------------------------------------------------------ training operators
 # The second library (include/zero/train.h); it is loaded at the first call.
-from .train import (ZERO_GLU_GELU, ZERO_GLU_SILU, ZERO_MAX_GROUPS, ZERO_STATE8_BLOCK,  # noqa: E402
-                    AdamGroup, Glu8Args, Linear8Args, TensorSet, XentArgs, rows8_stride,
+from .train import (ZERO_GLU_GELU, ZERO_GLU_SILU, ZERO_LINEAR8_BACKWARD,  # noqa: E402
+                    ZERO_LINEAR8_BACKWARD_ANY_DY, ZERO_LINEAR8_FORWARD, ZERO_MAX_GROUPS,
+                    ZERO_STATE8_BLOCK, AdamGroup, Glu8Args, Linear8Args, TensorSet, XentArgs, rows8_stride,
                     state8_blocks, zero_glu8_backward, zero_glu8_forward, zero_linear8_backward,
-                    zero_linear8_forward, zero_linear8_workspace_bytes, zero_rows8_decode,
-                    zero_rows8_encode, zero_state8_decode, zero_state8_encode,
-                    zero_tensors_apply, zero_tensors_norm, zero_tensors_plan,
-                    zero_tensors_scalars, zero_tensors_step, zero_xent_backward,
-                    zero_xent_forward, zero_xent_workspace_bytes)
+                    zero_linear8_forward, zero_linear8_workspace_bytes,
+                    zero_linear8_workspace_bytes_for, zero_rows8_decode, zero_rows8_encode,
+                    zero_state8_decode, zero_state8_encode, zero_tensors_apply,
+                    zero_tensors_norm, zero_tensors_plan, zero_tensors_scalars, zero_tensors_step,
+                    zero_xent_backward, zero_xent_forward, zero_xent_workspace_bytes)

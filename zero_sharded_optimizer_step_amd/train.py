@@ -570,6 +570,12 @@ def zero_glu8_backward(args: Glu8Args, stream=None) -> None:
 
 
 # ---------------------------------------------------------------- 8-bit products
+def zero_linear8_workspace_bytes_for(tokens: int, dim: int, out: int, uses: int) -> int:
+    """Bytes of workspace for calls of up to `tokens` tokens, of the uses named:
+    ZERO_LINEAR8_FORWARD, ZERO_LINEAR8_BACKWARD, ZERO_LINEAR8_BACKWARD_ANY_DY."""
+    return train_lib().zero_linear8_workspace_bytes_for(tokens, dim, out, uses)
+
+
 def zero_linear8_workspace_bytes(tokens: int, dim: int, out: int, forward: bool = True, backward: bool = True,
                                  any_dy: bool = True) -> int:
     """Bytes of workspace for calls of up to `tokens` tokens: of the forward,
@@ -580,7 +586,7 @@ def zero_linear8_workspace_bytes(tokens: int, dim: int, out: int, forward: bool 
         ((ZERO_LINEAR8_BACKWARD_ANY_DY if any_dy else ZERO_LINEAR8_BACKWARD) if backward else 0)
     if not uses:
         raise ValueError("a workspace for neither the forward nor the backward")
-    return train_lib().zero_linear8_workspace_bytes_for(tokens, dim, out, uses)
+    return zero_linear8_workspace_bytes_for(tokens, dim, out, uses)
 
 
 @dataclass
