@@ -97,7 +97,7 @@ int tensors_constants(const zero_tensors_args* a, bool peers, bool buffers, zero
 int check_xent_args(const zero_xent_args* a, bool backward) {
     if (!a) return fail(ZERO_EINVAL, "args is NULL");
     if (a->tokens < 0 || a->dim < 0 || a->vocab < 0) return fail(ZERO_EINVAL, "a size is negative");
-    const size_t need = zero_xent_workspace_bytes(a->tokens, a->dim, a->vocab);
+    const size_t need = xent_needs(a->tokens, a->dim, a->vocab);
     if (!need)
         return fail(ZERO_EINVAL, "tokens %lld, dim %lld, vocab %lld are out of range", (long long)a->tokens,
                     (long long)a->dim, (long long)a->vocab);

@@ -40,6 +40,8 @@ constexpr size_t kTensorsWorkspace = round_up(kSlotBytes, 256) + 256;
 int tensors_constants(const zero_tensors_args* a, bool peers, bool buffers, zero_tensors_scalars_t* k);
 
 int check_xent_args(const zero_xent_args* a, bool backward);
+// Bytes of workspace that calls of these sizes use; 0 for out-of-range ones.
+size_t xent_needs(int64_t tokens, int64_t dim, int64_t vocab);
 
 // x is what is encoded, or what codes are decoded into.
 int check_rows8(const void* x, int64_t x_stride, int32_t dtype, int64_t rows, int64_t dim, const void* codes,

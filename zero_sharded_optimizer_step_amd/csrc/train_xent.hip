@@ -601,6 +601,14 @@ int backward(const zero_xent_args* a, const Cut& c, hipStream_t st) {
 }
 
 }  // namespace
+
+size_t xent_needs(int64_t tokens, int64_t dim, int64_t vocab) {
+    // room for either layout of w
+    Cut whole, packed;
+    if (!cut(tokens, dim, vocab, false, &whole) || !cut(tokens, dim, vocab, true, &packed)) return 0;
+    return dim % 8 == 0 && whole.total > packed.total ? whole.total : packed.total;
+}
+
 }  // namespace zero
 
 using namespace zero;
@@ -608,10 +616,23 @@ using namespace zero;
 extern "C" {
 
 size_t zero_xent_workspace_bytes(int64_t tokens, int64_t dim, int64_t vocab) {
-    // room for either layout of w
-    Cut whole, packed;
-    if (!cut(tokens, dim, vocab, false, &whole) || !cut(tokens, dim, vocab, true, &packed)) return 0;
-    return dim % 8 == 0 && whole.total > packed.total ? whole.total : packed.total;
+    size_t most = xent_needs(tokens, dim, vocab);
+    if (!most) return 0;
+    // Fewer tokens may need more: they are cut into more slices, have wider
+    // pieces of the vocabulary or, few of them, more partials.  Between two of
+    // these numbers nothing but the tokens grows.
+    int64_t last = 0;
+    auto look = [&](int64_t t) {
+        if (t < 1 || t >= tokens || t == last) return;
+        last = t;
+        const size_t b = xent_needs(t, dim, vocab);
+        most = b > most ? b : most;
+    };
+    look(kFewTokens);
+    for (int64_t t = 128; t < tokens; t += 128) look(t);
+    for (const int64_t room : {kPBytes, kPackedBytes})
+        for (int64_t piece = 256; piece <= up(vocab, 256); piece += 256) look(room / 2 / piece);
+    return most;
 }
 
 int zero_xent_forward(const zero_xent_args* a, void* stream) {
